@@ -431,6 +431,145 @@ w4a16_status awq_fold_activations(const uint16_t* x, const float* s, uint16_t* x
                                   void* stream);
 
 /*
+ * Feed-forward operators around the W4A16 product.  A transformer layer's feed-forward half is
+ *     h = x + r;  y = rmsnorm(h) / s;  a = act(y . Wg^T) * (y . Wu^T);  out = a . Wd^T + h
+ * and the entry points below are its three steps, with their backward passes through frozen
+ * weights (the 4-bit codes have no gradient).  [AWQ translation, 3.2: 1 / s is folded into the
+ * preceding operator, which here is the norm.]
+ *
+ * Activations act(p), and act'(p) in the backward passes, in fp32:
+ *   NONE p;  RELU max(p, 0), derivative 0 at 0;  SILU p / (1 + e^-p);
+ *   GELU p (1 + erf(p / sqrt 2)) / 2;
+ *   GELU_TANH p (1 + tanh(sqrt(2 / pi) (p + 0.044715 p^3))) / 2.
+ */
+typedef enum {
+    W4A16_ACT_NONE = 0,
+    W4A16_ACT_RELU = 1,
+    W4A16_ACT_SILU = 2,
+    W4A16_ACT_GELU = 3,
+    W4A16_ACT_GELU_TANH = 4
+} w4a16_activation;
+
+/* The packed weights of one layer, as awq_quantize writes them (device pointers). */
+typedef struct {
+    const uint32_t* qweight; /* [N][K/8] */
+    const uint16_t* scales;  /* [K/group_size][N] fp16 bits */
+    const uint32_t* zeros;   /* [K/group_size][N/8] */
+} w4a16_weights;
+
+/*
+ * Workspace of the feed-forward operators: w4a16_fused_workspace_bytes(op, M, N, K) bytes for
+ * the current device, or 0 for invalid sizes.  N is F for the gated operators, and ignored (any
+ * value) for RMSNORM_BACKWARD.  The rules are those of w4a16_workspace_bytes: 16-byte aligned,
+ * zero-filled before its first use, left with the parts that must be zero zero-filled; one
+ * workspace of the largest size serves all calls of this library in stream order; calls that
+ * may overlap, replays of two captured graphs among them, need different workspaces.
+ */
+typedef enum {
+    W4A16_OP_LINEAR = 0,
+    W4A16_OP_LINEAR_BACKWARD = 1,
+    W4A16_OP_GATED = 2,
+    W4A16_OP_GATED_BACKWARD = 3,
+    W4A16_OP_RMSNORM_BACKWARD = 4
+} w4a16_fused_op;
+size_t w4a16_fused_workspace_bytes(int op, int64_t M, int64_t N, int64_t K);
+
+/*
+ * w4a16_linear_fused -- w4a16_linear_ex with bias, activation and residual in its epilogue:
+ *     p = x . dequant(Q)^T + bias;   y = bf16_rne( act(p) + residual )
+ *   bias      [N] bf16 bits, or NULL.   residual [M][N] bf16 bits, or NULL; it may be y itself
+ *             (the addition in place), otherwise y overlaps no input.
+ *   pre       [M][N] bf16 bits, output, or NULL: bf16_rne(p), for the backward pass.
+ *   activation: w4a16_activation.  group_size: as w4a16_linear_ex.
+ *   workspace: required, W4A16_OP_LINEAR.  M >= 1; M <= 16 runs the decode kernel, larger M
+ *   the tensor-core kernel, in which each weight is rounded once to bf16.  There is no CSR term.
+ *   Errors: NULL, SHAPE, ALIGN, VALUE (unknown activation), UNSUPPORTED when called.
+ */
+w4a16_status w4a16_linear_fused(const uint16_t* x, const w4a16_weights* weights, const uint16_t* bias,
+                                const uint16_t* residual, uint16_t* y, uint16_t* pre, int64_t M, int64_t N,
+                                int64_t K, int64_t group_size, int activation, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * w4a16_linear_fused_backward -- the gradients of w4a16_linear_fused:
+ *     dp = dy * act'(pre);   dx = bf16_rne( dp . dequant(Q) );   dbias = sum over tokens of dp
+ *   dy        [M][N] bf16 bits (also the residual's gradient).
+ *   pre       [M][N] bf16 bits, as the forward call wrote it.  Ignored, may be NULL, for NONE.
+ *   dx        [M][K] bf16 bits, output.  dbias [N] fp32, output, or NULL.
+ *   dp enters the product rounded to bf16 and the sum of dbias in fp32, unrounded.
+ *   workspace: required, W4A16_OP_LINEAR_BACKWARD.  Repeated calls give the same bits.
+ *   Errors: as w4a16_linear_fused.
+ */
+w4a16_status w4a16_linear_fused_backward(const uint16_t* dy, const uint16_t* pre, const w4a16_weights* weights,
+                                         uint16_t* dx, float* dbias, int64_t M, int64_t N, int64_t K,
+                                         int64_t group_size, int activation, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/*
+ * w4a16_gated -- the gated half of a feed-forward block, both projections in one kernel:
+ *     g = x . dequant(Qg)^T;  u = x . dequant(Qu)^T;   h = bf16_rne( act(g) * u )
+ *   x [M][K], h [M][F] bf16 bits; gate and up: two layers [F][K] of the same group_size.
+ *   g_out, u_out  [M][F] bf16 bits, outputs, or both NULL: bf16_rne(g), bf16_rne(u), for the
+ *                 backward pass.
+ *   workspace: required, W4A16_OP_GATED with N = F.  Otherwise as w4a16_linear_fused (NULL also
+ *   when only one of g_out and u_out is given).
+ */
+w4a16_status w4a16_gated(const uint16_t* x, const w4a16_weights* gate, const w4a16_weights* up, uint16_t* h,
+                         uint16_t* g_out, uint16_t* u_out, int64_t M, int64_t F, int64_t K, int64_t group_size,
+                         int activation, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * w4a16_gated_backward -- the gradient of w4a16_gated with respect to x:
+ *     dg = dh * u * act'(g);  du = dh * act(g);   dx = bf16_rne( dg . dequant(Qg) + du . dequant(Qu) )
+ *   dh, g, u [M][F] bf16 bits; dx [M][K] bf16 bits, output.  dg and du enter the product rounded
+ *   to bf16.  workspace: required, W4A16_OP_GATED_BACKWARD with N = F.  Errors: as w4a16_gated.
+ */
+w4a16_status w4a16_gated_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u,
+                                  const w4a16_weights* gate, const w4a16_weights* up, uint16_t* dx, int64_t M,
+                                  int64_t F, int64_t K, int64_t group_size, int activation, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * awq_rmsnorm -- residual addition, root-mean-square norm and the AWQ fold in one pass:
+ *     h = bf16_rne(x + residual);   y = bf16_rne( h * rsqrt(mean_k h^2 + eps) * weight / s )
+ *   x, residual, h, y [M][K] bf16 bits; weight [K] bf16 bits; s [K] fp32 (s_out of awq_quantize),
+ *   or NULL for no fold: y is then the norm itself.
+ *   residual  or NULL: h is then x.   h: output, or NULL when it is not wanted; it may be x or
+ *             residual (the addition in place).  y may be x or residual when h is another buffer.
+ *   The statistics and v = h * rstd * weight / s are fp32.
+ *   1 <= M <= 2^24; K a multiple of 8, 8 <= K <= 32768; eps finite and >= 0 (VALUE).  Every
+ *   pointer 16-byte aligned.  No workspace.
+ */
+w4a16_status awq_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
+                         float eps, uint16_t* h, uint16_t* y, int64_t M, int64_t K, void* stream);
+
+/*
+ * awq_rmsnorm_e4m3 -- awq_rmsnorm with its output in 8 bits: for each row, and each group of
+ * group_size channels of it, scale = max(max |v|, 1e-12) / 448 and q = e4m3_rne(v / scale), so
+ * that v is about q * scale (v as in awq_rmsnorm, fp32).
+ *   q [M][K] bytes (E4M3); scales [M][K/group_size] fp32.  group_size: K (one scale per row) or a
+ *   multiple of 128 that divides K.  A NaN in a group makes its scale and codes NaN; an infinity
+ *   makes the scale infinite, the infinite entries' codes NaN and the others 0.
+ *   Everything else as awq_rmsnorm.
+ */
+w4a16_status awq_rmsnorm_e4m3(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
+                              float eps, uint16_t* h, uint8_t* q, float* scales, int64_t M, int64_t K,
+                              int64_t group_size, void* stream);
+
+/*
+ * awq_rmsnorm_backward -- the gradients of awq_rmsnorm at h (the sum x + residual it wrote):
+ *     xhat = h * rstd;  v = dy * weight / s;   dx = bf16_rne( dh + rstd * (v - xhat * mean_k(v * xhat)) )
+ *     dweight = sum over rows of dy * xhat / s
+ *   dy, h, dx [M][K] bf16 bits; dh [M][K] bf16 bits, or NULL: the gradient that reaches h along the
+ *   residual stream.  dx is the gradient of x and of residual; it may be dy or dh.
+ *   dweight [K] fp32, output, or NULL.  weight, s, eps, M, K as in awq_rmsnorm.
+ *   workspace: required with dweight, W4A16_OP_RMSNORM_BACKWARD.  Repeated calls give the same bits.
+ */
+w4a16_status awq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* weight, const float* s,
+                                  const uint16_t* dh, float eps, uint16_t* dx, float* dweight, int64_t M,
+                                  int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * w4a16_selftest_timeout -- launch a one-thread kernel whose pipeline wait can never
  * complete and whose limit is limit_ns nanoseconds (0 .. 1e10; else W4A16_ERR_VALUE).  The
  * wait runs out through the same bounded-wait loop the kernels use, the kernel records a

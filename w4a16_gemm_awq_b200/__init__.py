@@ -17,6 +17,13 @@ mirror the C ABI in include/w4a16.h:
   gemv_plan(M, N, K, schedule)                  -> (schedule, cluster size, CTAs) the call would launch
   w4a16_gemm(...)                               -> y      (tcgen05 path, any M)
   workspace_bytes(M, N, K, csr=True)            -> bytes of zeroed device workspace a call needs
+  awq_rmsnorm(x, weight, residual, s)           -> (y, h)  residual addition, RMS norm and the 1/s fold
+  awq_rmsnorm_e4m3(...)                         -> (q, scales, h)  the same with an output in 8 bits
+  awq_rmsnorm_backward(dy, h, weight, s, dh)    -> (dx, dweight)
+  w4a16_linear_fused(x, qweight, scales, zeros, bias, residual, activation) -> y  (epilogue fused, any M)
+  w4a16_linear_fused_backward(dy, ...)          -> (dx, dbias)
+  w4a16_gated(x, gate, up, activation)          -> h = act(x gate^T) * (x up^T)  (any M)
+  w4a16_gated_backward(dh, g, u, gate, up)      -> dx
   check_device_status()                         -> raises W4A16Error on a recorded problem
 
 Bit containers: qweight [N][K/8] and zeros [K/128][N/8] are int32 tensors holding uint32
@@ -40,6 +47,8 @@ STATUS = {0: "W4A16_OK", 1: "W4A16_ERR_NULL", 2: "W4A16_ERR_SHAPE", 3: "W4A16_ER
           4: "W4A16_ERR_VALUE", 5: "W4A16_ERR_CUDA", 6: "W4A16_ERR_TIMEOUT", 7: "W4A16_ERR_UNSUPPORTED"}
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_VALUE, ERR_CUDA, ERR_TIMEOUT, ERR_UNSUPPORTED = range(8)
 GEMV_AUTO, GEMV_STREAM_K, GEMV_CLUSTER = range(3)
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+OP_LINEAR, OP_LINEAR_BACKWARD, OP_GATED, OP_GATED_BACKWARD, OP_RMSNORM_BACKWARD = range(5)
 
 
 class W4A16Error(RuntimeError):
@@ -51,6 +60,10 @@ class W4A16Error(RuntimeError):
 class Csr(ctypes.Structure):
     _fields_ = [("row_ptr", ctypes.c_void_p), ("col_idx", ctypes.c_void_p), ("values", ctypes.c_void_p),
                 ("nnz", ctypes.c_int64)]
+
+
+class Weights(ctypes.Structure):
+    _fields_ = [("qweight", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
 
 
 _lib = None
@@ -103,6 +116,16 @@ def lib() -> ctypes.CDLL:
         L.awq_search_alpha_workspace_bytes.argtypes = [I64, I64, I64, ctypes.c_int]
         L.awq_search_alpha_workspace_bytes.restype = ctypes.c_size_t
         L.awq_fold_activations.argtypes = [P, P, P, I64, I64, P]
+        PW, CI, SZ = ctypes.POINTER(Weights), ctypes.c_int, ctypes.c_size_t
+        L.w4a16_fused_workspace_bytes.argtypes = [CI, I64, I64, I64]
+        L.w4a16_fused_workspace_bytes.restype = SZ
+        L.w4a16_linear_fused.argtypes = [P, PW, P, P, P, P, I64, I64, I64, I64, CI, P, SZ, P]
+        L.w4a16_linear_fused_backward.argtypes = [P, P, PW, P, P, I64, I64, I64, I64, CI, P, SZ, P]
+        L.w4a16_gated.argtypes = [P, PW, PW, P, P, P, I64, I64, I64, I64, CI, P, SZ, P]
+        L.w4a16_gated_backward.argtypes = [P, P, P, PW, PW, P, I64, I64, I64, I64, CI, P, SZ, P]
+        L.awq_rmsnorm.argtypes = [P, P, P, P, F, P, P, I64, I64, P]
+        L.awq_rmsnorm_e4m3.argtypes = [P, P, P, P, F, P, P, P, I64, I64, I64, P]
+        L.awq_rmsnorm_backward.argtypes = [P, P, P, P, P, F, P, P, I64, I64, P, SZ, P]
         L.w4a16_status_string.argtypes = [ctypes.c_int]
         L.w4a16_status_string.restype = ctypes.c_char_p
         L.w4a16_version.argtypes = []
@@ -475,6 +498,247 @@ def awq_split_outliers_workspace_bytes(N: int, K: int) -> int:
 
 def awq_search_alpha_workspace_bytes(M: int, N: int, K: int, n_alpha: int) -> int:
     return int(lib().awq_search_alpha_workspace_bytes(M, N, K, int(n_alpha)))
+
+
+# ---- feed-forward operators ----------------------------------------------------------------
+
+# The counters at the front of a workspace: the part that must be zero when a call starts.
+_WORKSPACE_ZERO_BYTES = (1 << 22) // 128 * 4
+
+
+def w4a16_fused_workspace_bytes(op: int, M: int, N: int, K: int) -> int:
+    """Bytes of workspace a feed-forward operator (OP_LINEAR, ...; N = F for the gated ones) needs
+    on the current device."""
+    return int(lib().w4a16_fused_workspace_bytes(int(op), M, N, K))
+
+
+def _expect(t, dtype, shape, name, device):
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _layer(w, K, group_size, name, device):
+    """(Weights, N) of a layer's (qweight, scales, zeros), its shapes checked against K."""
+    qw, sc, z = w
+    if qw.dim() != 2:
+        raise ValueError(f"{name}: qweight must be a matrix")
+    N, gs = qw.shape[0], int(group_size)
+    if gs < 1 or K % gs != 0 or K % 8 != 0:
+        raise ValueError(f"{name}: group size {gs} does not divide K = {K}")
+    _expect(qw, torch.int32, (N, K // 8), f"{name} qweight", device)
+    _expect(sc, torch.int16, (K // gs, N), f"{name} scales", device)
+    _expect(z, torch.int32, (K // gs, N // 8), f"{name} zeros", device)
+    return Weights(qw.data_ptr(), sc.data_ptr(), z.data_ptr()), N
+
+
+def _rows(t, name):
+    if t.dim() != 2 or t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA bfloat16 matrix, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.shape
+
+
+def _activation(a) -> int:
+    if isinstance(a, str):
+        if a not in ACTIVATIONS:
+            raise ValueError(f"activation {a!r}: expected one of {sorted(ACTIVATIONS)}")
+        return ACTIVATIONS[a]
+    return int(a)
+
+
+def _output(out, dtype, shape, name, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _expect(out, dtype, shape, name, device)
+    return out
+
+
+def _data(t):
+    return t.data_ptr() if t is not None else None
+
+
+class _device_of:
+    """Makes a tensor's device the current one for a call, where it is not already."""
+
+    def __init__(self, device):
+        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+_fused_bytes = {}
+
+
+def _fused_workspace(ws, device, op, M, N, K):
+    """The caller's workspace, or the cached one of the current stream.  While the stream is being
+    captured, one of the graph's own, its counters zeroed by the graph: graphs share none, and a
+    later call that needs a larger one takes nothing from under a graph."""
+    if ws is not None:
+        if ws.device != device or not ws.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on {device}")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+    key = (device.index, op, M, N, K)
+    nbytes = _fused_bytes.get(key)
+    if nbytes is None:
+        nbytes = _fused_bytes[key] = w4a16_fused_workspace_bytes(op, M, N, K)
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        ws[:_WORKSPACE_ZERO_BYTES].zero_()
+    else:
+        ws = workspace(device, nbytes)
+    return ws.data_ptr(), ws.numel()
+
+
+def w4a16_linear_fused(x, qweight, scales, zeros, bias=None, residual=None, activation="none", group_size=128,
+                       out=None, pre_out=None, workspace=None):
+    """y = bf16(act(x . dequant(Q)^T + bias) + residual), fused in the product's epilogue.  bias bf16
+    [N]; residual bf16 [M][N], which may be out; pre_out bf16 [M][N], if given, receives the value
+    before the activation (for the backward pass)."""
+    M, K = _rows(x, "x")
+    dev = x.device
+    w, N = _layer((qweight, scales, zeros), K, group_size, "weights", dev)
+    if bias is not None:
+        _expect(bias, torch.bfloat16, (N,), "bias", dev)
+    if residual is not None:
+        _expect(residual, torch.bfloat16, (M, N), "residual", dev)
+    if pre_out is not None:
+        _expect(pre_out, torch.bfloat16, (M, N), "pre_out", dev)
+    act = _activation(activation)
+    with _device_of(dev):
+        y = _output(out, torch.bfloat16, (M, N), "out", dev)
+        ws, wsb = _fused_workspace(workspace, dev, OP_LINEAR, M, N, K)
+        _check(lib().w4a16_linear_fused(x.data_ptr(), w, _data(bias), _data(residual), y.data_ptr(), _data(pre_out),
+                                        M, N, K, int(group_size), act, ws, wsb, _stream(dev)), "w4a16_linear_fused")
+    return y
+
+
+def w4a16_linear_fused_backward(dy, qweight, scales, zeros, pre=None, activation="none", group_size=128,
+                                bias_grad=False, out=None, workspace=None):
+    """(dx bf16 [M][K], dbias fp32 [N] or None) of w4a16_linear_fused from dy bf16 [M][N]; pre is
+    what the forward call wrote to pre_out (not needed without an activation).  dy is the
+    residual's gradient."""
+    M, N = _rows(dy, "dy")
+    dev = dy.device
+    if qweight.dim() != 2 or qweight.shape[0] != N:
+        raise ValueError(f"qweight {tuple(qweight.shape)} does not match dy {tuple(dy.shape)}")
+    K = qweight.shape[1] * 8
+    w, _ = _layer((qweight, scales, zeros), K, group_size, "weights", dev)
+    act = _activation(activation)
+    if act != 0 and pre is None:
+        raise ValueError("pre: needed for the gradient of an activation")
+    if pre is not None:
+        _expect(pre, torch.bfloat16, (M, N), "pre", dev)
+    with _device_of(dev):
+        dx = _output(out, torch.bfloat16, (M, K), "out", dev)
+        db = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
+        ws, wsb = _fused_workspace(workspace, dev, OP_LINEAR_BACKWARD, M, N, K)
+        _check(lib().w4a16_linear_fused_backward(dy.data_ptr(), _data(pre), w, dx.data_ptr(), _data(db), M, N, K,
+                                                 int(group_size), act, ws, wsb, _stream(dev)),
+               "w4a16_linear_fused_backward")
+    return dx, db
+
+
+def w4a16_gated(x, gate, up, activation="silu", group_size=128, out=None, save=False, workspace=None):
+    """h = bf16(act(x . dequant(gate)^T) * (x . dequant(up)^T)) in one kernel; gate and up are
+    (qweight, scales, zeros) of two layers [F][K].  save: returns (h, g, u), with the two projections
+    in bf16 for the backward pass."""
+    M, K = _rows(x, "x")
+    dev = x.device
+    wg, F = _layer(gate, K, group_size, "gate", dev)
+    wu, Fu = _layer(up, K, group_size, "up", dev)
+    if F != Fu:
+        raise ValueError(f"gate has {F} output channels, up has {Fu}")
+    act = _activation(activation)
+    with _device_of(dev):
+        h = _output(out, torch.bfloat16, (M, F), "out", dev)
+        g = torch.empty(M, F, dtype=torch.bfloat16, device=dev) if save else None
+        u = torch.empty(M, F, dtype=torch.bfloat16, device=dev) if save else None
+        ws, wsb = _fused_workspace(workspace, dev, OP_GATED, M, F, K)
+        _check(lib().w4a16_gated(x.data_ptr(), wg, wu, h.data_ptr(), _data(g), _data(u), M, F, K, int(group_size), act,
+                                 ws, wsb, _stream(dev)), "w4a16_gated")
+    return (h, g, u) if save else h
+
+
+def w4a16_gated_backward(dh, g, u, gate, up, activation="silu", group_size=128, out=None, workspace=None):
+    """dx bf16 [M][K] of w4a16_gated from dh bf16 [M][F] and the g, u that it saved."""
+    M, F = _rows(dh, "dh")
+    dev = dh.device
+    _expect(g, torch.bfloat16, (M, F), "g", dev)
+    _expect(u, torch.bfloat16, (M, F), "u", dev)
+    K = gate[0].shape[-1] * 8
+    wg, Fg = _layer(gate, K, group_size, "gate", dev)
+    wu, Fu = _layer(up, K, group_size, "up", dev)
+    if Fg != F or Fu != F:
+        raise ValueError(f"gate and up have {Fg} and {Fu} output channels, dh has {F}")
+    act = _activation(activation)
+    with _device_of(dev):
+        dx = _output(out, torch.bfloat16, (M, K), "out", dev)
+        ws, wsb = _fused_workspace(workspace, dev, OP_GATED_BACKWARD, M, F, K)
+        _check(lib().w4a16_gated_backward(dh.data_ptr(), g.data_ptr(), u.data_ptr(), wg, wu, dx.data_ptr(), M, F, K,
+                                          int(group_size), act, ws, wsb, _stream(dev)), "w4a16_gated_backward")
+    return dx
+
+
+def _norm_operands(x, weight, residual, s):
+    M, K = _rows(x, "x")
+    _expect(weight, torch.bfloat16, (K,), "weight", x.device)
+    if residual is not None:
+        _expect(residual, torch.bfloat16, (M, K), "residual", x.device)
+    if s is not None:
+        _expect(s, torch.float32, (K,), "s", x.device)
+    return M, K, x.device
+
+
+def awq_rmsnorm(x, weight, residual=None, s=None, eps=1e-6, out=None, sum_out=None):
+    """(y, h): h = bf16(x + residual), written to sum_out (a new tensor by default; x or residual for
+    the addition in place), and y = bf16(h * rsqrt(mean h^2 + eps) * weight / s).  Without a
+    residual h is x itself, unless sum_out is given."""
+    M, K, dev = _norm_operands(x, weight, residual, s)
+    with _device_of(dev):
+        y = _output(out, torch.bfloat16, (M, K), "out", dev)
+        h = None if residual is None and sum_out is None else _output(sum_out, torch.bfloat16, (M, K), "sum_out", dev)
+        _check(lib().awq_rmsnorm(x.data_ptr(), _data(residual), weight.data_ptr(), _data(s), eps, _data(h),
+                                 y.data_ptr(), M, K, _stream(dev)), "awq_rmsnorm")
+    return y, x if h is None else h
+
+
+def awq_rmsnorm_e4m3(x, weight, residual=None, s=None, eps=1e-6, group_size=0, out=None, scales_out=None, sum_out=None):
+    """(q, scales, h): awq_rmsnorm with its output in 8 bits: q float8_e4m3fn [M][K] and scales fp32
+    [M][K/group_size], the output being about q * scale.  group_size 0: one scale per row."""
+    M, K, dev = _norm_operands(x, weight, residual, s)
+    gs = int(group_size) or K
+    if gs < 1 or K % gs != 0:
+        raise ValueError(f"group size {gs} does not divide K = {K}")
+    with _device_of(dev):
+        q = _output(out, torch.float8_e4m3fn, (M, K), "out", dev)
+        sc = _output(scales_out, torch.float32, (M, K // gs), "scales_out", dev)
+        h = None if residual is None and sum_out is None else _output(sum_out, torch.bfloat16, (M, K), "sum_out", dev)
+        _check(lib().awq_rmsnorm_e4m3(x.data_ptr(), _data(residual), weight.data_ptr(), _data(s), eps, _data(h),
+                                      q.data_ptr(), sc.data_ptr(), M, K, gs, _stream(dev)), "awq_rmsnorm_e4m3")
+    return q, sc, x if h is None else h
+
+
+def awq_rmsnorm_backward(dy, h, weight, s=None, dh=None, eps=1e-6, weight_grad=True, out=None, workspace=None):
+    """(dx bf16 [M][K], dweight fp32 [K] or None) of awq_rmsnorm at the sum h; dh, if given, is the
+    gradient that reaches h along the residual stream.  dx is the gradient of x and of residual."""
+    M, K, dev = _norm_operands(dy, weight, h, s)
+    if dh is not None:
+        _expect(dh, torch.bfloat16, (M, K), "dh", dev)
+    with _device_of(dev):
+        dx = _output(out, torch.bfloat16, (M, K), "out", dev)
+        dw, ws, wsb = None, None, 0
+        if weight_grad:
+            dw = torch.empty(K, dtype=torch.float32, device=dev)
+            ws, wsb = _fused_workspace(workspace, dev, OP_RMSNORM_BACKWARD, M, 0, K)
+        _check(lib().awq_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _data(s), _data(dh), eps,
+                                          dx.data_ptr(), _data(dw), M, K, ws, wsb, _stream(dev)), "awq_rmsnorm_backward")
+    return dx, dw
 
 
 w4a16_workspace_bytes = workspace_bytes

@@ -1,0 +1,67 @@
+// act.cuh -- the activations of the feed-forward operators and their derivatives, in fp32.
+//
+//   SILU       p sg(p);                derivative sg + p sg (1 - sg),   sg(p) = 1 / (1 + e^-p)
+//   GELU       p Phi(p);               derivative Phi + p phi,          Phi = (1 + erf(p / sqrt 2)) / 2
+//   GELU_TANH  p (1 + tanh z) / 2 = p sg(2 z), z = sqrt(2 / pi) (p + 0.044715 p^3);
+//              derivative sg + p sg (1 - sg) 2 z'
+// The sigmoid is 1 / (1 + e^-p) by the fast exponential and division (relative error below 2^-20,
+// far inside the bf16 rounding that every result goes through).  It saturates without a NaN: e^-p
+// overflows to infinity for p below -88 and 1 / inf is 0, and p * 0 is 0 for every finite p.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "w4a16.h"
+
+namespace w4a16 {
+
+__device__ __forceinline__ float sigmoid_fast(float p) { return __fdividef(1.0f, 1.0f + __expf(-p)); }
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float p) {
+    if constexpr (ACT == W4A16_ACT_RELU) return p > 0.0f ? p : (p == p ? 0.0f : p);
+    if constexpr (ACT == W4A16_ACT_SILU) return p * sigmoid_fast(p);
+    if constexpr (ACT == W4A16_ACT_GELU) return 0.5f * p * (1.0f + erff(p * 0.70710678118654752f));
+    if constexpr (ACT == W4A16_ACT_GELU_TANH)
+        return p * sigmoid_fast(1.5957691216057308f * fmaf(0.044715f * p * p, p, p));
+    return p;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_grad(float p) {
+    if constexpr (ACT == W4A16_ACT_RELU) return p > 0.0f ? 1.0f : 0.0f;
+    if constexpr (ACT == W4A16_ACT_SILU) {
+        const float sg = sigmoid_fast(p);
+        return fmaf(p * sg, 1.0f - sg, sg);
+    }
+    if constexpr (ACT == W4A16_ACT_GELU)
+        return fmaf(p * 0.39894228040143268f, __expf(-0.5f * p * p), 0.5f * (1.0f + erff(p * 0.70710678118654752f)));
+    if constexpr (ACT == W4A16_ACT_GELU_TANH) {
+        const float sg = sigmoid_fast(1.5957691216057308f * fmaf(0.044715f * p * p, p, p));
+        return fmaf(p * sg, (1.0f - sg) * 1.5957691216057308f * fmaf(0.134145f * p, p, 1.0f), sg);
+    }
+    return 1.0f;
+}
+
+// The activation as a run-time value, where it costs nothing against the rest of the kernel.
+__device__ __forceinline__ float act_value(int act, float p) {
+    switch (act) {
+        case W4A16_ACT_RELU: return act_value<W4A16_ACT_RELU>(p);
+        case W4A16_ACT_SILU: return act_value<W4A16_ACT_SILU>(p);
+        case W4A16_ACT_GELU: return act_value<W4A16_ACT_GELU>(p);
+        case W4A16_ACT_GELU_TANH: return act_value<W4A16_ACT_GELU_TANH>(p);
+        default: return p;
+    }
+}
+
+__device__ __forceinline__ float act_grad(int act, float p) {
+    switch (act) {
+        case W4A16_ACT_RELU: return act_grad<W4A16_ACT_RELU>(p);
+        case W4A16_ACT_SILU: return act_grad<W4A16_ACT_SILU>(p);
+        case W4A16_ACT_GELU: return act_grad<W4A16_ACT_GELU>(p);
+        case W4A16_ACT_GELU_TANH: return act_grad<W4A16_ACT_GELU_TANH>(p);
+        default: return 1.0f;
+    }
+}
+
+}  // namespace w4a16

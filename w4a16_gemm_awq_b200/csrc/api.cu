@@ -348,6 +348,64 @@ SearchLayout search_layout(int64_t M, int64_t N, int64_t K, int n_alpha, int num
 
 constexpr int kMaxAlphas = 64;
 
+// ---------------------------------------------------------------------------------------
+// Feed-forward operators.
+constexpr int64_t kMaxNormK = 32768;
+
+bool valid_activation(int act) { return act >= W4A16_ACT_NONE && act <= W4A16_ACT_GELU_TANH; }
+
+bool valid_layer_shape(int64_t M, int64_t N, int64_t K) {
+    return M >= 1 && M <= kMaxM && N >= 128 && N % 128 == 0 && N <= kMaxN && K >= 1024 && K % 1024 == 0 && K <= kMaxK;
+}
+
+bool valid_group_size(int64_t gs, int64_t K) { return gs >= 128 && gs % 128 == 0 && gs <= K && K % gs == 0; }
+
+// Checks a layer's packed weights (a host struct of device pointers).
+w4a16_status take_weights(const w4a16_weights* w, PackedWeights* out) {
+    if (!w || !w->qweight || !w->scales || !w->zeros) return W4A16_ERR_NULL;
+    *out = PackedWeights{w->qweight, w->scales, w->zeros};
+    return W4A16_OK;
+}
+
+bool weights_aligned(const PackedWeights& w) {
+    return aligned(w.qweight, 16) && aligned(w.scales, 16) && aligned(w.zeros, 16);
+}
+
+// Workspace of the backward passes: the counter region, then
+//   dp [M][N] bf16 (gated: dg and du), then the partial column sums of dbias.
+size_t backward_dp_bytes(int64_t M, int64_t N) { return up256((size_t)M * (size_t)N * 2); }
+
+size_t fused_bytes(int op, int64_t M, int64_t N, int64_t K, int num_sms) {
+    switch (op) {
+        case W4A16_OP_LINEAR: return kCounterRegionBytes;
+        case W4A16_OP_LINEAR_BACKWARD:
+            return kCounterRegionBytes + backward_dp_bytes(M, N) + up256((size_t)linear_dp_blocks(M) * N * 4);
+        case W4A16_OP_GATED: return kCounterRegionBytes;
+        case W4A16_OP_GATED_BACKWARD: return kCounterRegionBytes + 2 * backward_dp_bytes(M, N);
+        case W4A16_OP_RMSNORM_BACKWARD:
+            return kCounterRegionBytes + up256((size_t)rmsnorm_backward_rows(M, (int)K, num_sms) * K * 4);
+        default: return 0;
+    }
+}
+
+// Checks the caller's workspace against fused_bytes and returns its part after the counters.
+w4a16_status take_fused_workspace(int op, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                                  DeviceInfo** d, uint8_t** after) {
+    if (!workspace) return W4A16_ERR_NULL;
+    if (!aligned(workspace, 16)) return W4A16_ERR_ALIGN;
+    w4a16_status st = device_info(d);
+    if (st != W4A16_OK) return st;
+    if (workspace_bytes < fused_bytes(op, M, N, K, (*d)->num_sms)) return W4A16_ERR_SHAPE;
+    *after = static_cast<uint8_t*>(workspace) + kCounterRegionBytes;
+    return W4A16_OK;
+}
+
+w4a16_status validate_norm(int64_t M, int64_t K, float eps) {
+    if (M < 1 || M > kMaxM || K < 8 || K % 8 != 0 || K > kMaxNormK) return W4A16_ERR_SHAPE;
+    if (!std::isfinite(eps) || eps < 0.0f) return W4A16_ERR_VALUE;
+    return W4A16_OK;
+}
+
 }  // namespace
 }  // namespace w4a16
 
@@ -707,6 +765,190 @@ w4a16_status awq_fold_activations(const uint16_t* x, const float* s, uint16_t* x
     w4a16_status st = device_info(&d);
     if (st != W4A16_OK) return st;
     return from_cuda(launch_search_fold(x, s, x_out, (int)M, (int)K, static_cast<cudaStream_t>(stream)));
+}
+
+size_t w4a16_fused_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
+    if (op < W4A16_OP_LINEAR || op > W4A16_OP_RMSNORM_BACKWARD) return 0;
+    if (op == W4A16_OP_RMSNORM_BACKWARD ? validate_norm(M, K, 0.0f) != W4A16_OK : !valid_layer_shape(M, N, K)) return 0;
+    DeviceInfo* d = nullptr;
+    if (device_info(&d) != W4A16_OK) return 0;
+    return fused_bytes(op, M, N, K, d->num_sms);
+}
+
+w4a16_status w4a16_linear_fused(const uint16_t* x, const w4a16_weights* weights, const uint16_t* bias,
+                                const uint16_t* residual, uint16_t* y, uint16_t* pre, int64_t M, int64_t N,
+                                int64_t K, int64_t group_size, int activation, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    FfnArgs a{};
+    if (!x || !y) return W4A16_ERR_NULL;
+    w4a16_status st = take_weights(weights, &a.w);
+    if (st != W4A16_OK) return st;
+    if (!valid_layer_shape(M, N, K) || !valid_group_size(group_size, K)) return W4A16_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(pre, 16) ||
+        !weights_aligned(a.w))
+        return W4A16_ERR_ALIGN;
+    if (!valid_activation(activation)) return W4A16_ERR_VALUE;
+    DeviceInfo* d = nullptr;
+    uint8_t* ws = nullptr;
+    st = take_fused_workspace(W4A16_OP_LINEAR, M, N, K, workspace, workspace_bytes, &d, &ws);
+    if (st != W4A16_OK) return st;
+    a.a = x;
+    a.bias = bias;
+    a.residual = residual;
+    a.y = y;
+    a.pre = pre;
+    a.M = M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.group_size = (int)group_size;
+    a.act = activation;
+    return from_cuda(launch_ffn(a, false, false, static_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_linear_fused_backward(const uint16_t* dy, const uint16_t* pre, const w4a16_weights* weights,
+                                         uint16_t* dx, float* dbias, int64_t M, int64_t N, int64_t K,
+                                         int64_t group_size, int activation, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    FfnArgs a{};
+    if (!dy || !dx || (activation != W4A16_ACT_NONE && !pre)) return W4A16_ERR_NULL;
+    w4a16_status st = take_weights(weights, &a.w);
+    if (st != W4A16_OK) return st;
+    if (!valid_layer_shape(M, N, K) || !valid_group_size(group_size, K)) return W4A16_ERR_SHAPE;
+    if (!aligned(dy, 16) || !aligned(dx, 16) || !aligned(dbias, 16) ||
+        (activation != W4A16_ACT_NONE && !aligned(pre, 16)) || !weights_aligned(a.w))
+        return W4A16_ERR_ALIGN;
+    if (!valid_activation(activation)) return W4A16_ERR_VALUE;
+    DeviceInfo* d = nullptr;
+    uint8_t* ws = nullptr;
+    st = take_fused_workspace(W4A16_OP_LINEAR_BACKWARD, M, N, K, workspace, workspace_bytes, &d, &ws);
+    if (st != W4A16_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool act = activation != W4A16_ACT_NONE;
+    uint16_t* dp = act ? reinterpret_cast<uint16_t*>(ws) : nullptr;
+    float* sums = reinterpret_cast<float*>(ws + backward_dp_bytes(M, N));
+    if (act || dbias) {
+        st = from_cuda(launch_linear_dp(dy, pre, dp, dbias, sums, M, (int)N, activation, s));
+        if (st != W4A16_OK) return st;
+    }
+    a.a = act ? dp : dy;
+    a.y = dx;
+    a.M = M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.group_size = (int)group_size;
+    return from_cuda(launch_ffn(a, true, false, s));
+}
+
+w4a16_status w4a16_gated(const uint16_t* x, const w4a16_weights* gate, const w4a16_weights* up, uint16_t* h,
+                         uint16_t* g_out, uint16_t* u_out, int64_t M, int64_t F, int64_t K, int64_t group_size,
+                         int activation, void* workspace, size_t workspace_bytes, void* stream) {
+    FfnArgs a{};
+    if (!x || !h || (g_out == nullptr) != (u_out == nullptr)) return W4A16_ERR_NULL;
+    w4a16_status st = take_weights(gate, &a.w);
+    if (st == W4A16_OK) st = take_weights(up, &a.w2);
+    if (st != W4A16_OK) return st;
+    if (!valid_layer_shape(M, F, K) || F > kMaxN / 2 || !valid_group_size(group_size, K)) return W4A16_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(h, 16) || !aligned(g_out, 16) || !aligned(u_out, 16) || !weights_aligned(a.w) ||
+        !weights_aligned(a.w2))
+        return W4A16_ERR_ALIGN;
+    if (!valid_activation(activation)) return W4A16_ERR_VALUE;
+    DeviceInfo* d = nullptr;
+    uint8_t* ws = nullptr;
+    st = take_fused_workspace(W4A16_OP_GATED, M, F, K, workspace, workspace_bytes, &d, &ws);
+    if (st != W4A16_OK) return st;
+    a.a = x;
+    a.y = h;
+    a.pre = g_out;
+    a.pre2 = u_out;
+    a.M = M;
+    a.N = (int)F;
+    a.K = (int)K;
+    a.group_size = (int)group_size;
+    a.act = activation;
+    return from_cuda(launch_ffn(a, false, true, static_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_gated_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u,
+                                  const w4a16_weights* gate, const w4a16_weights* up, uint16_t* dx, int64_t M,
+                                  int64_t F, int64_t K, int64_t group_size, int activation, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    FfnArgs a{};
+    if (!dh || !g || !u || !dx) return W4A16_ERR_NULL;
+    w4a16_status st = take_weights(gate, &a.w);
+    if (st == W4A16_OK) st = take_weights(up, &a.w2);
+    if (st != W4A16_OK) return st;
+    if (!valid_layer_shape(M, F, K) || F > kMaxN / 2 || !valid_group_size(group_size, K)) return W4A16_ERR_SHAPE;
+    if (!aligned(dh, 16) || !aligned(g, 16) || !aligned(u, 16) || !aligned(dx, 16) || !weights_aligned(a.w) ||
+        !weights_aligned(a.w2))
+        return W4A16_ERR_ALIGN;
+    if (!valid_activation(activation)) return W4A16_ERR_VALUE;
+    DeviceInfo* d = nullptr;
+    uint8_t* ws = nullptr;
+    st = take_fused_workspace(W4A16_OP_GATED_BACKWARD, M, F, K, workspace, workspace_bytes, &d, &ws);
+    if (st != W4A16_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint16_t* dg = reinterpret_cast<uint16_t*>(ws);
+    uint16_t* du = reinterpret_cast<uint16_t*>(ws + backward_dp_bytes(M, F));
+    st = from_cuda(launch_gated_dp(dh, g, u, dg, du, M, (int)F, activation, d->num_sms, s));
+    if (st != W4A16_OK) return st;
+    a.a = dg;
+    a.a2 = du;
+    a.y = dx;
+    a.M = M;
+    a.N = (int)F;
+    a.K = (int)K;
+    a.group_size = (int)group_size;
+    return from_cuda(launch_ffn(a, true, true, s));
+}
+
+w4a16_status awq_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
+                         float eps, uint16_t* h, uint16_t* y, int64_t M, int64_t K, void* stream) {
+    if (!x || !weight || !y) return W4A16_ERR_NULL;
+    w4a16_status st = validate_norm(M, K, eps);
+    if (st != W4A16_OK) return st;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(s, 16) || !aligned(h, 16) ||
+        !aligned(y, 16))
+        return W4A16_ERR_ALIGN;
+    DeviceInfo* d = nullptr;
+    st = device_info(&d);
+    if (st != W4A16_OK) return st;
+    return from_cuda(launch_rmsnorm(x, residual, weight, s, eps, h, y, nullptr, nullptr, 0, M, (int)K, d->num_sms,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status awq_rmsnorm_e4m3(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
+                              float eps, uint16_t* h, uint8_t* q, float* scales, int64_t M, int64_t K,
+                              int64_t group_size, void* stream) {
+    if (!x || !weight || !q || !scales) return W4A16_ERR_NULL;
+    w4a16_status st = validate_norm(M, K, eps);
+    if (st != W4A16_OK) return st;
+    if (group_size != K && (group_size < 128 || group_size % 128 != 0 || K % group_size != 0)) return W4A16_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(s, 16) || !aligned(h, 16) ||
+        !aligned(q, 16) || !aligned(scales, 16))
+        return W4A16_ERR_ALIGN;
+    DeviceInfo* d = nullptr;
+    st = device_info(&d);
+    if (st != W4A16_OK) return st;
+    return from_cuda(launch_rmsnorm(x, residual, weight, s, eps, h, nullptr, q, scales, (int)group_size, M, (int)K,
+                                    d->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status awq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* weight, const float* s,
+                                  const uint16_t* dh, float eps, uint16_t* dx, float* dweight, int64_t M,
+                                  int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!dy || !h || !weight || !dx) return W4A16_ERR_NULL;
+    w4a16_status st = validate_norm(M, K, eps);
+    if (st != W4A16_OK) return st;
+    if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(s, 16) || !aligned(dh, 16) ||
+        !aligned(dx, 16) || !aligned(dweight, 16))
+        return W4A16_ERR_ALIGN;
+    DeviceInfo* d = nullptr;
+    uint8_t* ws = nullptr;
+    st = dweight ? take_fused_workspace(W4A16_OP_RMSNORM_BACKWARD, M, 0, K, workspace, workspace_bytes, &d, &ws)
+                 : device_info(&d);
+    if (st != W4A16_OK) return st;
+    return from_cuda(launch_rmsnorm_backward(dy, h, weight, s, dh, eps, dx, dweight, reinterpret_cast<float*>(ws), M,
+                                             (int)K, d->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 w4a16_status w4a16_selftest_quotient(uint64_t* mismatches, uint32_t first[4], void* stream) {

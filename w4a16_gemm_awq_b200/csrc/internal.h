@@ -145,4 +145,47 @@ cudaError_t launch_gemm(const GemmMaps& maps, const GemmPlan& plan, int group_ra
                         const uint32_t* zeros, const float* ysp, int ysp_ld, uint16_t* y, float* partials,
                         unsigned* counters, int M, int N, int K, unsigned* err, cudaStream_t stream);
 
+// ------------------------------------------------------------------ feed-forward operators --
+
+// y = bf16(v) (q == nullptr), or q and scales per `group` channels (y == nullptr); see rmsnorm.cu.
+cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
+                           float eps, uint16_t* h, uint16_t* y, uint8_t* q, float* scales, int group, int64_t M, int K,
+                           int num_sms, cudaStream_t stream);
+
+// partials: rmsnorm_backward_rows x K fp32, used with dweight.
+int rmsnorm_backward_rows(int64_t M, int K, int num_sms);
+cudaError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* weight, const float* s,
+                                    const uint16_t* dh, float eps, uint16_t* dx, float* dweight, float* partials,
+                                    int64_t M, int K, int num_sms, cudaStream_t stream);
+
+// The packed weights of a layer (w4a16_weights by value).
+struct PackedWeights {
+    const uint32_t* qweight;
+    const uint16_t* scales;
+    const uint32_t* zeros;
+};
+
+// A feed-forward product (see ffn.cu).  Forward: a = x [M][K], outputs [M][N].  Backward: a (and
+// a2) [M][N], output y [M][K].  w2, pre2 and a2 belong to the gated forms.
+struct FfnArgs {
+    const uint16_t* a;
+    const uint16_t* a2;
+    PackedWeights w, w2;
+    const uint16_t* bias;
+    const uint16_t* residual;
+    uint16_t* y;
+    uint16_t* pre;
+    uint16_t* pre2;
+    int64_t M;
+    int N, K, group_size, act;
+};
+cudaError_t launch_ffn(const FfnArgs& a, bool back, bool two, cudaStream_t stream);
+
+// The elementwise steps of the backward passes.  sums: linear_dp_blocks(M) x N fp32, used with dbias.
+int linear_dp_blocks(int64_t M);
+cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* dbias, float* sums,
+                             int64_t M, int N, int act, cudaStream_t stream);
+cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dg, uint16_t* du,
+                            int64_t M, int F, int act, int num_sms, cudaStream_t stream);
+
 }  // namespace w4a16
