@@ -64,4 +64,24 @@ __device__ __forceinline__ float act_grad(int act, float p) {
     }
 }
 
+// The activation of C values held in registers, the choice made once for all of them: a choice per
+// value makes C copies of every activation's code, which then comes from the instruction cache's
+// misses (a GEMM epilogue of 32 values took 6000 cycles that way).
+template <int C, int ACT>
+__device__ __forceinline__ void act_each(float (&v)[C]) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = act_value<ACT>(v[i]);
+}
+
+template <int C>
+__device__ __forceinline__ void act_values(int act, float (&v)[C]) {
+    switch (act) {
+        case W4A16_ACT_RELU: act_each<C, W4A16_ACT_RELU>(v); break;
+        case W4A16_ACT_SILU: act_each<C, W4A16_ACT_SILU>(v); break;
+        case W4A16_ACT_GELU: act_each<C, W4A16_ACT_GELU>(v); break;
+        case W4A16_ACT_GELU_TANH: act_each<C, W4A16_ACT_GELU_TANH>(v); break;
+        default: break;
+    }
+}
+
 }  // namespace w4a16

@@ -371,21 +371,37 @@ bool weights_aligned(const PackedWeights& w) {
     return aligned(w.qweight, 16) && aligned(w.scales, 16) && aligned(w.zeros, 16);
 }
 
-// Workspace of the backward passes: the counter region, then
-//   dp [M][N] bf16 (gated: dg and du), then the partial column sums of dbias.
+// The product's launch for an operator: output channels and contraction of all its weights.
+FfnPlan plan_of(int op, int64_t M, int64_t N, int64_t K, int num_sms) {
+    switch (op) {
+        case W4A16_OP_LINEAR: return ffn_plan(M, (int)N, (int)(K / 128), num_sms);
+        case W4A16_OP_GATED: return ffn_plan(M, (int)(2 * N), (int)(K / 128), num_sms);
+        case W4A16_OP_LINEAR_BACKWARD: return ffn_plan(M, (int)K, (int)(N / 128), num_sms);
+        default: return ffn_plan(M, (int)K, (int)(2 * (N / 128)), num_sms);
+    }
+}
+
+// Whether an operator's forward product runs the decode GEMV (rows: output channels, 2 F gated).
+bool decodes(int op, int64_t M, int64_t N, int64_t K, int num_sms) {
+    if ((op != W4A16_OP_LINEAR && op != W4A16_OP_GATED) || M > 16 || K > gemv_max_k()) return false;
+    const int64_t rows = op == W4A16_OP_GATED ? 2 * N : N;
+    return gemv_fits((int)rows, (int)K, num_sms);
+}
+
+// Workspace of the feed-forward operators: the counter region, then the product's fp32 partial
+// tiles; for the backward passes then dp [M][N] bf16 (gated: dg and du), then the partial column
+// sums of dbias.  For the norm's backward pass the partial sums of dweight follow the counters.
 size_t backward_dp_bytes(int64_t M, int64_t N) { return up256((size_t)M * (size_t)N * 2); }
 
 size_t fused_bytes(int op, int64_t M, int64_t N, int64_t K, int num_sms) {
-    switch (op) {
-        case W4A16_OP_LINEAR: return kCounterRegionBytes;
-        case W4A16_OP_LINEAR_BACKWARD:
-            return kCounterRegionBytes + backward_dp_bytes(M, N) + up256((size_t)linear_dp_blocks(M) * N * 4);
-        case W4A16_OP_GATED: return kCounterRegionBytes;
-        case W4A16_OP_GATED_BACKWARD: return kCounterRegionBytes + 2 * backward_dp_bytes(M, N);
-        case W4A16_OP_RMSNORM_BACKWARD:
-            return kCounterRegionBytes + up256((size_t)rmsnorm_backward_rows(M, (int)K, num_sms) * K * 4);
-        default: return 0;
-    }
+    if (op == W4A16_OP_RMSNORM_BACKWARD)
+        return kCounterRegionBytes + up256((size_t)rmsnorm_backward_rows(M, (int)K, num_sms) * K * 4);
+    if (decodes(op, M, N, K, num_sms)) return kCounterRegionBytes + gemv_partial_bytes(num_sms);
+    const size_t b = kCounterRegionBytes + up256(plan_of(op, M, N, K, num_sms).partial_bytes);
+    if (op == W4A16_OP_LINEAR_BACKWARD)
+        return b + backward_dp_bytes(M, N) + up256((size_t)linear_dp_blocks(M) * N * 4);
+    if (op == W4A16_OP_GATED_BACKWARD) return b + 2 * backward_dp_bytes(M, N);
+    return b;
 }
 
 // Checks the caller's workspace against fused_bytes and returns its part after the counters.
@@ -398,6 +414,82 @@ w4a16_status take_fused_workspace(int op, int64_t M, int64_t N, int64_t K, void*
     if (workspace_bytes < fused_bytes(op, M, N, K, (*d)->num_sms)) return W4A16_ERR_SHAPE;
     *after = static_cast<uint8_t*>(workspace) + kCounterRegionBytes;
     return W4A16_OK;
+}
+
+// Tensor map of row-major bf16 activations [rows][cols] in boxes of 64 columns x box_rows.
+w4a16_status encode_rows(EncodeTiledFn enc, CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t cols, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? W4A16_OK
+               : W4A16_ERR_CUDA;
+}
+
+// Tensor map of qweight [N][K/8] in boxes of 16 words (128 codes) x 64 rows.
+w4a16_status encode_packed(EncodeTiledFn enc, CUtensorMap* map, const uint32_t* p, int64_t N, int64_t K) {
+    const cuuint64_t dims[2] = {(cuuint64_t)(K / 8), (cuuint64_t)N};
+    const cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
+    const cuuint32_t box[2] = {16, 64};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint32_t*>(p), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? W4A16_OK
+               : W4A16_ERR_CUDA;
+}
+
+// The decode GEMV of a feed-forward operator; ws: the workspace after its counters.
+w4a16_status run_ffn_decode(int op, const FfnArgs& a, const DeviceInfo& d, void* workspace, uint8_t* ws,
+                            cudaStream_t stream) {
+    const bool gated = op == W4A16_OP_GATED;
+    const int rows = gated ? 2 * a.N : a.N;
+    const GemvPlan plan = gemv_plan((int)a.M, rows, a.K, d.num_sms, W4A16_GEMV_AUTO, gated);
+    EncodeTiledFn enc = nullptr;
+    w4a16_status st = encoder(&enc);
+    if (st != W4A16_OK) return st;
+    GemvMaps maps;
+    for (int i = 0; i < (gated ? 2 : 1); ++i) {
+        const cuuint64_t dims[3] = {16, (cuuint64_t)a.N, (cuuint64_t)(a.K / 128)};
+        const cuuint64_t strides[2] = {(cuuint64_t)a.K / 2, 64};
+        const cuuint32_t box[3] = {16, (cuuint32_t)(gated ? 64 : 128), 4};
+        const cuuint32_t estr[3] = {1, 1, 1};
+        if (enc(i ? &maps.w2 : &maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3,
+                const_cast<uint32_t*>(i ? a.w2.qweight : a.w.qweight), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return W4A16_ERR_CUDA;
+    }
+    const GemvEpilogue e{gated ? kGemvGated : kGemvLinear, a.act, a.bias, a.residual, a.pre, a.pre2,
+                         a.w2.scales, a.w2.zeros};
+    return from_cuda(launch_gemv(maps, plan, a.group_size / 128, a.a, a.w.scales, a.w.zeros, nullptr, a.y,
+                                 reinterpret_cast<float*>(ws), static_cast<unsigned*>(workspace), (int)a.M, rows, a.K,
+                                 d.status, stream, 4, &e));
+}
+
+// The product of a feed-forward operator; ws: the workspace after its counters.
+w4a16_status run_ffn(int op, const FfnArgs& a, const DeviceInfo& d, void* workspace, uint8_t* ws, cudaStream_t stream) {
+    const bool back = op == W4A16_OP_LINEAR_BACKWARD || op == W4A16_OP_GATED_BACKWARD;
+    const bool two = op == W4A16_OP_GATED || op == W4A16_OP_GATED_BACKWARD;
+    if (decodes(op, a.M, a.N, a.K, d.num_sms)) return run_ffn_decode(op, a, d, workspace, ws, stream);
+    const FfnPlan plan = plan_of(op, a.M, a.N, a.K, d.num_sms);
+    if (plan.tiles > INT_MAX / 2) return W4A16_ERR_UNSUPPORTED;  // 32-bit tile indexes
+    EncodeTiledFn enc = nullptr;
+    w4a16_status st = encoder(&enc);
+    if (st != W4A16_OK) return st;
+    FfnMaps maps;
+    st = encode_rows(enc, &maps.x, a.a, a.M, back ? a.N : a.K, plan.bn / 2);
+    maps.x2 = maps.x;
+    if (st == W4A16_OK && a.a2 != nullptr) st = encode_rows(enc, &maps.x2, a.a2, a.M, a.N, plan.bn / 2);
+    if (st == W4A16_OK) st = encode_packed(enc, &maps.w, a.w.qweight, a.N, a.K);
+    maps.w2 = maps.w;
+    if (st == W4A16_OK && two) st = encode_packed(enc, &maps.w2, a.w2.qweight, a.N, a.K);
+    if (st != W4A16_OK) return st;
+    return from_cuda(launch_ffn_gemm(maps, plan, a, back, two, reinterpret_cast<float*>(ws),
+                                     static_cast<unsigned*>(workspace), d.status, stream));
 }
 
 w4a16_status validate_norm(int64_t M, int64_t K, float eps) {
@@ -802,7 +894,7 @@ w4a16_status w4a16_linear_fused(const uint16_t* x, const w4a16_weights* weights,
     a.K = (int)K;
     a.group_size = (int)group_size;
     a.act = activation;
-    return from_cuda(launch_ffn(a, false, false, static_cast<cudaStream_t>(stream)));
+    return run_ffn(W4A16_OP_LINEAR, a, *d, workspace, ws, static_cast<cudaStream_t>(stream));
 }
 
 w4a16_status w4a16_linear_fused_backward(const uint16_t* dy, const uint16_t* pre, const w4a16_weights* weights,
@@ -824,8 +916,9 @@ w4a16_status w4a16_linear_fused_backward(const uint16_t* dy, const uint16_t* pre
     if (st != W4A16_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool act = activation != W4A16_ACT_NONE;
-    uint16_t* dp = act ? reinterpret_cast<uint16_t*>(ws) : nullptr;
-    float* sums = reinterpret_cast<float*>(ws + backward_dp_bytes(M, N));
+    uint8_t* grads = ws + up256(plan_of(W4A16_OP_LINEAR_BACKWARD, M, N, K, d->num_sms).partial_bytes);
+    uint16_t* dp = act ? reinterpret_cast<uint16_t*>(grads) : nullptr;
+    float* sums = reinterpret_cast<float*>(grads + backward_dp_bytes(M, N));
     if (act || dbias) {
         st = from_cuda(launch_linear_dp(dy, pre, dp, dbias, sums, M, (int)N, activation, s));
         if (st != W4A16_OK) return st;
@@ -836,7 +929,7 @@ w4a16_status w4a16_linear_fused_backward(const uint16_t* dy, const uint16_t* pre
     a.N = (int)N;
     a.K = (int)K;
     a.group_size = (int)group_size;
-    return from_cuda(launch_ffn(a, true, false, s));
+    return run_ffn(W4A16_OP_LINEAR_BACKWARD, a, *d, workspace, ws, s);
 }
 
 w4a16_status w4a16_gated(const uint16_t* x, const w4a16_weights* gate, const w4a16_weights* up, uint16_t* h,
@@ -865,7 +958,7 @@ w4a16_status w4a16_gated(const uint16_t* x, const w4a16_weights* gate, const w4a
     a.K = (int)K;
     a.group_size = (int)group_size;
     a.act = activation;
-    return from_cuda(launch_ffn(a, false, true, static_cast<cudaStream_t>(stream)));
+    return run_ffn(W4A16_OP_GATED, a, *d, workspace, ws, static_cast<cudaStream_t>(stream));
 }
 
 w4a16_status w4a16_gated_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u,
@@ -887,8 +980,9 @@ w4a16_status w4a16_gated_backward(const uint16_t* dh, const uint16_t* g, const u
     st = take_fused_workspace(W4A16_OP_GATED_BACKWARD, M, F, K, workspace, workspace_bytes, &d, &ws);
     if (st != W4A16_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint16_t* dg = reinterpret_cast<uint16_t*>(ws);
-    uint16_t* du = reinterpret_cast<uint16_t*>(ws + backward_dp_bytes(M, F));
+    uint8_t* grads = ws + up256(plan_of(W4A16_OP_GATED_BACKWARD, M, F, K, d->num_sms).partial_bytes);
+    uint16_t* dg = reinterpret_cast<uint16_t*>(grads);
+    uint16_t* du = reinterpret_cast<uint16_t*>(grads + backward_dp_bytes(M, F));
     st = from_cuda(launch_gated_dp(dh, g, u, dg, du, M, (int)F, activation, d->num_sms, s));
     if (st != W4A16_OK) return st;
     a.a = dg;
@@ -898,7 +992,7 @@ w4a16_status w4a16_gated_backward(const uint16_t* dh, const uint16_t* g, const u
     a.N = (int)F;
     a.K = (int)K;
     a.group_size = (int)group_size;
-    return from_cuda(launch_ffn(a, true, true, s));
+    return run_ffn(W4A16_OP_GATED_BACKWARD, a, *d, workspace, ws, s);
 }
 
 w4a16_status awq_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,

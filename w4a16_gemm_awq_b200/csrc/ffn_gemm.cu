@@ -1,0 +1,655 @@
+// ffn_gemm.cu -- the feed-forward products for more than a few tokens, on the 5th-generation tensor
+// cores (tcgen05 over CTA pairs, TMEM, TMA).
+//
+//   LINEAR    y[m][n] = bf16( act( sum_k x[m][k] w[n][k] + bias[n] ) + residual[m][n] )
+//   GATED     h[m][f] = bf16( act( sum_k x[m][k] wg[f][k] ) * sum_k x[m][k] wu[f][k] )
+//   BACKWARD  dx[m][k] = bf16( sum_n dp[m][n] w[n][k] (+ sum_n dp2[m][n] w2[n][k]) )
+//   w = bf16((q - z) scale), rounded once.
+//
+// Design (B200):
+//   - A CTA pair computes a tile of 256 output channels x BN tokens (BN a multiple of 32 up to 256)
+//     with tcgen05.mma.cta_group::2 (M = 256: 128 channels in each CTA's TMEM).  Each CTA stages its
+//     own 128 dequantized weight rows and half of the tokens: half the L2 and shared-memory traffic
+//     per product of a single-CTA tile of the same width.
+//   - The two accumulators (BN fp32 columns each, at TMEM columns 0 and 256) are used in turn, so the
+//     epilogue of one tile runs while the next one accumulates.
+//   - Warp roles (512 threads): 0 TMA of the activations, 1 MMA issue (leader CTA), 2 TMA of the
+//     packed weights, 3 TMEM allocation, 4-7 epilogue (one TMEM lane quarter each), 8-15 dequant:
+//     two groups of four warps, which take the stages of 64 contraction steps in turn.
+//   - Dequant.  A ring entry holds the packed weights of 128 x 128 codes (8 KB, 64-byte rows, 64-byte
+//     swizzle).  A thread turns 8 words into 64 bf16 and stores them as 16-byte chunks of the A stage
+//     in the layout that the MMA reads, conflict-free.  Forward products contract over k, so a packed
+//     row becomes a row of A (K-major).  The backward product contracts over n, so a packed row
+//     becomes a column of A: it is stored as it lies and the MMA reads A channel-major (MN-major).
+//   - One rounding per weight at two multiplications: with scale = hi + lo, hi = bf16(scale), lo has
+//     at most 3 bits and (q - z) 4, so (q - z) lo is exact in bf16 and fma(q - z, hi, (q - z) lo) is
+//     the correctly rounded product.
+//   - GATED interleaves gate and up rows in sixteens, so the two sums of a channel sit in one warp's
+//     lanes l and l + 16 and meet by a shuffle.
+//   - Whole tiles go round the pairs; the tiles that do not fill a round are cut along the contraction
+//     into equal runs, one per pair, whose fp32 partial tiles meet in the workspace: the last to arrive
+//     adds them in the order of the runs, so the bits do not depend on which that is.  The cut tiles
+//     come first, so that joining them hides behind whole tiles.  No pair waits for another.
+//   - Every wait is bounded; one that runs out records kErrTimeout and its role stops.  All roles of
+//     both CTAs then meet at the closing cluster barrier, since each of their waits is bounded too.
+#include <algorithm>
+#include <cmath>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "internal.h"
+
+namespace w4a16 {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kS = 6;                    // stages of 64 contraction steps
+constexpr int kP = 4;                    // packed entries of 128 contraction steps
+constexpr int kABytes = 128 * 128;       // 128 channels x 64 steps, bf16
+constexpr int kBBytes = 128 * 128;       // up to 128 tokens (this CTA's half) x 64 steps, bf16
+constexpr int kEntryBytes = 128 * 64;    // 128 packed rows of 16 words
+constexpr int kParBytes = 512;           // their 128 scales (256 bytes) and 16 words of zero points
+constexpr int kAOff = 0;
+constexpr int kBOff = kAOff + kS * kABytes;
+constexpr int kPOff = kBOff + kS * kBBytes;
+constexpr int kParOff = kPOff + kP * kEntryBytes;
+constexpr int kBarOff = kParOff + kP * kParBytes;
+constexpr int kSmemBytes = kBarOff + 256;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemSecond = 256;    // columns of the second accumulator
+
+enum { kLinear = 0, kGated = 1, kBackward = 2 };
+
+struct GemmArgs2 {
+    PackedWeights w, w2;
+    const uint16_t* bias;
+    const uint16_t* residual;
+    uint16_t* y;
+    uint16_t* pre;
+    uint16_t* pre2;
+    float* partials;
+    unsigned* counters;
+    unsigned* err;
+    int M, N, K;       // N: rows of one weight matrix
+    int gr;            // group size / 128
+    int act;
+    int bn;            // tokens per tile
+    int entries;       // contraction / 128, both matrices of a gated backward product together
+    int entries1;      // entries of the first matrix
+    int tiles_c;       // tiles along the output channels
+    int tiles;
+    int cut;           // tiles 0 .. cut - 1 are cut into runs
+    int runs;          // runs over the cut tiles' entries
+};
+
+// Unit u of `units`, cut into `runs` equal runs: run p starts at p * units / runs.
+__device__ __forceinline__ int run_begin(int p, int units, int runs) { return (int)((long long)units * p / runs); }
+__device__ __forceinline__ int run_of(int u, int units, int runs) {
+    return (int)((((long long)u + 1) * runs - 1) / units);
+}
+
+// A pair's pieces of work in order: its run over the cut tiles, tile by tile, then its whole tiles.
+struct Walk {
+    int u, u_end;   // rest of the run
+    int whole;      // next whole tile
+    int tile, e0, e1;
+    bool partial;   // the tile has several contributors
+    int first, count, index;  // of those: the first run, how many, this one's place
+};
+
+__device__ __forceinline__ Walk walk_start(const GemmArgs2& p, int pair) {
+    Walk w;
+    const int units = p.cut * p.entries;
+    w.u = w.u_end = 0;
+    if (pair < p.runs) {
+        w.u = run_begin(pair, units, p.runs);
+        w.u_end = run_begin(pair + 1, units, p.runs);
+    }
+    w.whole = p.cut + pair;
+    w.first = w.index = 0;
+    w.count = 1;
+    return w;
+}
+
+__device__ __forceinline__ bool walk_step(Walk& w, const GemmArgs2& p, int pair, int pairs) {
+    if (w.u < w.u_end) {
+        const int units = p.cut * p.entries;
+        w.tile = w.u / p.entries;
+        const int t0 = w.tile * p.entries;
+        w.e0 = w.u - t0;
+        w.e1 = min(w.u_end, t0 + p.entries) - t0;
+        w.u = t0 + w.e1;
+        w.first = run_of(t0, units, p.runs);
+        w.count = run_of(t0 + p.entries - 1, units, p.runs) - w.first + 1;
+        w.index = pair - w.first;
+        w.partial = w.count > 1;
+        return true;
+    }
+    if (w.whole < p.tiles) {
+        w.tile = w.whole;
+        w.whole += pairs;
+        w.e0 = 0;
+        w.e1 = p.entries;
+        w.partial = false;
+        return true;
+    }
+    return false;
+}
+
+// Shared-memory operand descriptors, 128-byte swizzle.  K-major: rows of 128 bytes, 8-row groups 1024
+// bytes apart.  MN-major: 64 channels x 8 steps in 1024 bytes; the next 8 steps 1024 bytes on, the next
+// 64 channels 8192 bytes on.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading, uint32_t stride) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on the barrier at this offset in both CTAs of the pair when the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+        : "memory");
+}
+
+// TMA tile into this CTA's shared memory that completes on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b),
+                                     *reinterpret_cast<__nv_bfloat162*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Arrive on a barrier of either CTA of the pair.  What it announces is either in the async proxy's view
+// already (the writers' proxy fence) or in TMEM (tcgen05 fences), so CTA-scope release is enough; the
+// cluster-scope form costs a memory barrier per stage (gated, 4096 tokens, K 4096, F 14336: 1444 us
+// with it, 1122 us without, before the changes that came after).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A row's scale and zero point in one group, as the dequant needs them.
+struct RowParams {
+    uint32_t hi, lo, zero;  // bf16 pairs: scale's leading part, its rest, 128 + z
+};
+
+__device__ __forceinline__ RowParams row_params(uint16_t scale, uint32_t z) {
+    const float s = fp16_bits_to_float(scale);
+    const uint32_t hi = float_to_bf16_bits(s);
+    const uint32_t lo = float_to_bf16_bits(s - bf16_bits_to_float((uint16_t)hi));
+    return RowParams{hi | (hi << 16), lo | (lo << 16), 0x43004300u | z | (z << 16)};
+}
+
+// The 8 weights of a packed word as bf16, in element order.
+__device__ __forceinline__ uint4 dequant_word(uint32_t word, const RowParams& r) {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t t;
+        asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(t) : "r"(word >> (4 * i)), "r"(0x000F000Fu), "r"(0x43004300u));
+        t = bf16x2_sub(t, r.zero);
+        v[i] = bf16x2_fma(t, r.hi, bf16x2_mul(t, r.lo));
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// The whole warp waits; the result is the same in all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+
+// Barrier among the four epilogue warps.
+__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_x2,
+                const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_w2,
+                const GemmArgs2 p) {
+    // Pointers derive from the array itself, so that the compiler keeps the shared address space.
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {  // the swizzled stages need 1024-byte alignment
+        if (threadIdx.x == 0) record_error(p.err, kErrShape);
+        return;
+    }
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);  // leader: activations landed, weights written
+    uint64_t* empty = full + kS;     // the MMAs have read the stage
+    uint64_t* pfull = empty + kS;    // a packed entry has landed
+    uint64_t* pempty = pfull + kP;   // the dequant warps have read it
+    uint64_t* dfull = pempty + kP;   // an accumulator is complete
+    uint64_t* dempty = dfull + 2;    // leader: both CTAs' epilogues have read it
+    uint64_t* drain = dempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    int* last_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+    // From blockIdx and a broadcast, so that the compiler sees them as the same in a whole warp.
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const int rank = (int)(blockIdx.x & 1);
+    const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+    const int half_bn = p.bn >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kS; ++i) {
+            mbar_init(&full[i], 1 + 8);  // the leader's expected bytes, four dequant warps of each CTA
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kP; ++i) {
+            mbar_init(&pfull[i], 1);
+            mbar_init(&pempty[i], 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dempty[i], 8);  // four epilogue warps of each CTA
+        }
+        mbar_init(drain, 1);
+        fence_mbarrier_init();
+    }
+    if (warp == 3) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // the other CTA's barriers are initialised too
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+
+    auto fail = [&]() { record_error(p.err, kErrTimeout); };
+    Walk w = walk_start(p, pair);
+
+    // The TMA and MMA warps run their loops as whole warps and issue from one elected lane: the operands
+    // of those instructions sit in uniform registers, and a loop that one lane runs alone moves each of
+    // them there every time (385 to 480 cycles to issue a stage's four MMAs).
+    if (warp == 0) {
+        // ---------------------------------------------------------------- activations
+        prefetch_tensormap(&map_x);
+        bool ok = true;
+        unsigned s = 0;
+        while (ok && walk_step(w, p, pair, pairs)) {
+            const int m0 = (w.tile / p.tiles_c) * p.bn + rank * half_bn;
+            for (int c = 2 * w.e0; c < 2 * w.e1; ++c, ++s) {
+                const unsigned slot = s % kS;
+                if (s >= kS && !warp_wait(&empty[slot], (s / kS - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)p.bn * 128u);
+                    const bool second = MODE == kBackward && c >= 2 * p.entries1;
+                    tma_load_2d_pair(smem + kBOff + slot * kBBytes, second ? &map_x2 : &map_x,
+                                     cluster_map(&full[slot], 0), (second ? c - 2 * p.entries1 : c) * 64, m0);
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && lane == 0) fail();
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- packed weights
+        prefetch_tensormap(&map_w);
+        bool ok = true;
+        unsigned i = 0;
+        while (ok && walk_step(w, p, pair, pairs)) {
+            const int tc = w.tile % p.tiles_c;
+            for (int e = w.e0; e < w.e1; ++e, ++i) {
+                const unsigned slot = i % kP;
+                if (i >= kP && !warp_wait(&pempty[slot], (i / kP - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* dst = smem + kPOff + slot * kEntryBytes;
+                uint8_t* par = smem + kParOff + slot * kParBytes;
+                // 64 packed rows from n with their scales and zero points, to half hh of the entry
+                auto load = [&](int hh, const CUtensorMap* map, const PackedWeights& q, int word, int n, int g) {
+                    tma_load_2d(dst + hh * (kEntryBytes / 2), map, &pfull[slot], word, n);
+                    bulk_load(par + 128 * hh, q.scales + (size_t)g * p.N + n, 128, &pfull[slot]);
+                    bulk_load(par + 256 + 32 * hh, q.zeros + (size_t)g * (p.N >> 3) + (n >> 3), 32, &pfull[slot]);
+                };
+                if (elect_one()) {
+                    if (MODE == kLinear) {
+                        // the last pair's second half may be past N: its rows go nowhere
+                        const int n = tc * 256 + rank * 128;
+                        const bool in = n < p.N;
+                        mbar_arrive_expect_tx(&pfull[slot], in ? kEntryBytes + 320 : 16);
+                        if (in) {
+                            load(0, &map_w, p.w, e * 16, n, e / p.gr);
+                            load(1, &map_w, p.w, e * 16, n + 64, e / p.gr);
+                        } else {
+                            bulk_load(par, p.w.scales, 16, &pfull[slot]);
+                        }
+                    } else if (MODE == kGated) {
+                        const int n = tc * 128 + rank * 64;
+                        mbar_arrive_expect_tx(&pfull[slot], kEntryBytes + 320);
+                        load(0, &map_w, p.w, e * 16, n, e / p.gr);
+                        load(1, &map_w2, p.w2, e * 16, n, e / p.gr);
+                    } else {
+                        const bool second = e >= p.entries1;
+                        const CUtensorMap* map = second ? &map_w2 : &map_w;
+                        const PackedWeights& q = second ? p.w2 : p.w;
+                        const int n = (second ? e - p.entries1 : e) * 128, kt = tc * 2 + rank;
+                        mbar_arrive_expect_tx(&pfull[slot], kEntryBytes + 320);
+                        load(0, map, q, kt * 16, n, kt / p.gr);
+                        load(1, map, q, kt * 16, n + 64, kt / p.gr);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && lane == 0) fail();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issue
+        if (rank == 0) {
+            // D fp32, A and B bf16, B K-major, A K-major or (backward) MN-major, M = 256, N = bn
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (MODE == kBackward ? 1u << 15 : 0u) |
+                                   ((uint32_t)(p.bn >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+            const uint32_t a0 = smem_u32(smem) + kAOff, b0 = smem_u32(smem) + kBOff;
+            bool ok = true;
+            unsigned s = 0;
+            for (unsigned t = 0; ok && walk_step(w, p, pair, pairs); ++t) {
+                const unsigned buf = t & 1;
+                const uint32_t d = tmem + buf * kTmemSecond;
+                if (t >= 2 && !warp_wait(&dempty[buf], (t / 2 - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                for (int c = 2 * w.e0; c < 2 * w.e1; ++c, ++s) {
+                    const unsigned slot = s % kS;
+                    if (!warp_wait(&full[slot], (s / kS) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = a0 + slot * kABytes, b = b0 + slot * kBBytes;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint64_t ad = MODE == kBackward ? smem_desc(a + kk * 2048, 8192, 1024)
+                                                                  : smem_desc(a + kk * 32, 16, 1024);
+                            mma_pair(d, ad, smem_desc(b + kk * 32, 16, 1024), idesc, (c > 2 * w.e0 || kk > 0) ? 1u : 0u);
+                        }
+                        commit_pair(&empty[slot]);
+                        if (c == 2 * w.e1 - 1) commit_pair(&dfull[buf]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) {
+                if (lane == 0) fail();
+                if (elect_one()) commit_pair(drain);  // MMAs in flight finish first
+                (void)warp_wait(drain, 0);
+            }
+        }
+    } else if (warp >= 8) {
+        // ---------------------------------------------------------------- dequant
+        const int group = (warp - 8) >> 2;          // takes stage 2 e + group of entry e
+        const int t = threadIdx.x & 127;
+        // forward: row t of A (for GATED 16 gate rows, 16 up rows, ...), half `group` of its 64 bytes;
+        // backward: step t % 64 of the stage, channels 64 (t / 64) .. + 63
+        const int prow = MODE == kLinear ? t
+                         : MODE == kGated ? ((t >> 4) & 1) * 64 + 16 * (t >> 5) + (t & 15)
+                                          : 64 * group + (t & 63);
+        const int half = MODE == kBackward ? t >> 6 : group;
+        const uint32_t src0 = prow * 64 + (((2 * half) ^ ((prow >> 1) & 3)) << 4);
+        const uint32_t src1 = prow * 64 + (((2 * half + 1) ^ ((prow >> 1) & 3)) << 4);
+        const int arow = MODE == kBackward ? (t & 63) : t;   // 128-byte row of the A stage
+        const uint32_t dst = (MODE == kBackward ? half * 8192 : 0) + arow * 128;
+        const uint32_t sw = (arow & 7) << 4;
+        bool ok = true;
+        unsigned i = 0;  // packed entries so far; stage 2 i + group
+        while (ok && walk_step(w, p, pair, pairs)) {
+            for (int e = w.e0; e < w.e1; ++e, ++i) {
+                const unsigned ps = i % kP;
+                if (!warp_wait(&pfull[ps], (i / kP) & 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint8_t* src = smem + kPOff + ps * kEntryBytes;
+                const uint4 wa = *reinterpret_cast<const uint4*>(src + src0);
+                const uint4 wb = *reinterpret_cast<const uint4*>(src + src1);
+                const uint8_t* par = smem + kParOff + ps * kParBytes;
+                const uint16_t sbits = reinterpret_cast<const uint16_t*>(par)[prow];
+                const uint32_t zword = reinterpret_cast<const uint32_t*>(par + 256)[prow >> 3] >> (4 * (prow & 7));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pempty[ps]);
+                const RowParams rp = row_params(sbits, zword & 15u);
+                const unsigned s = 2 * i + group, slot = s % kS;
+                if (s >= kS && !warp_wait(&empty[slot], (s / kS - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* a = smem + kAOff + slot * kABytes + dst;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(a + ((c << 4) ^ sw)) = dequant_word(c < 4 ? u4_get(wa, c) : u4_get(wb, c - 4), rp);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(cluster_map(&full[slot], 0));
+            }
+        }
+        if (!ok && lane == 0) fail();
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------------- epilogue
+        const int quarter = warp & 3;
+        const int row = 32 * quarter + lane;  // TMEM lane
+        const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
+        bool ok = true;
+        for (unsigned t = 0; walk_step(w, p, pair, pairs); ++t) {
+            const unsigned buf = t & 1;
+            if (!warp_wait(&dfull[buf], (t / 2) & 1)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + t_lane + buf * kTmemSecond;
+            const int tc = w.tile % p.tiles_c;
+            const int m0 = (w.tile / p.tiles_c) * p.bn;
+            const int mlim = min(p.bn, p.M - m0);  // tokens of this tile
+            // partial tiles, token-major: [run + tile][rank][bn][128]
+            float* part0 = p.partials + ((size_t)(w.first + w.tile) * 2 + rank) * p.bn * 128 + row;
+            const size_t part_step = (size_t)2 * p.bn * 128;
+            if (w.partial) {
+                float* mine = part0 + w.index * part_step;
+#pragma unroll 1
+                for (int c0 = 0; c0 < mlim; c0 += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(d + (uint32_t)c0, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) __stcg(mine + (size_t)(c0 + j) * 128, __uint_as_float(r[j]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(cluster_map(&dempty[buf], 0));
+                // the partial tile is published by the counter; the last to count itself joins all
+                __threadfence();
+                epilogue_barrier();
+                if (warp == 4 && lane == 0) {
+                    unsigned* counter = p.counters + 2 * w.tile + rank;
+                    const bool last = atomic_add_acq_rel_gpu(counter, 1u) == (unsigned)(w.count - 1);
+                    if (last) atomicExch(counter, 0u);
+                    *last_flag = last;
+                }
+                epilogue_barrier();
+                const bool last = *reinterpret_cast<volatile int*>(last_flag) != 0;
+                epilogue_barrier();
+                if (!last) continue;
+                __threadfence();
+            }
+            const int n = MODE == kLinear ? tc * 256 + rank * 128 + row
+                          : MODE == kGated ? tc * 128 + rank * 64 + 16 * quarter + (lane & 15)
+                                           : tc * 256 + rank * 128 + row;
+            const int ld = MODE == kBackward ? p.K : p.N;
+            const bool in = n < ld;
+            float bias = 0.0f;
+            if (MODE == kLinear && p.bias != nullptr && in) bias = bf16_bits_to_float(p.bias[n]);
+#pragma unroll 1
+            for (int c0 = 0; c0 < mlim; c0 += 32) {
+                float acc[32];
+                if (w.partial) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[j] = __ldcg(part0 + (size_t)(c0 + j) * 128);
+                    for (int q = 1; q < w.count; ++q)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[j] += __ldcg(part0 + q * part_step + (size_t)(c0 + j) * 128);
+                } else {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(d + (uint32_t)c0, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[j] = __uint_as_float(r[j]);
+                }
+                const int nj = mlim - c0;  // valid columns of this chunk (32 or more: all)
+                const size_t o0 = (size_t)(m0 + c0) * ld + n;
+                if constexpr (MODE == kGated) {
+                    if (p.pre != nullptr) {
+                        uint16_t* o = (lane < 16 ? p.pre : p.pre2) + o0;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < nj) o[(size_t)j * ld] = float_to_bf16_bits(acc[j]);
+                    }
+                    // lanes below 16 finish tokens 0..15 of the chunk, the others 16..31
+                    const bool low = lane < 16;
+                    const int j0 = low ? 0 : 16;
+                    float g[16], u[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float got = __shfl_xor_sync(0xffffffffu, low ? acc[j + 16] : acc[j], 16);
+                        g[j] = low ? acc[j] : got;
+                        u[j] = low ? got : acc[j + 16];
+                    }
+                    act_values(p.act, g);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j0 + j < nj) p.y[o0 + (size_t)(j0 + j) * ld] = float_to_bf16_bits(g[j] * u[j]);
+                } else if (in) {
+                    if constexpr (MODE == kLinear) {
+                        uint16_t res[32];
+                        if (p.residual != nullptr) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                res[j] = j < nj ? p.residual[o0 + (size_t)j * ld] : (uint16_t)0;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[j] += bias;
+                        if (p.pre != nullptr) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j < nj) p.pre[o0 + (size_t)j * ld] = float_to_bf16_bits(acc[j]);
+                        }
+                        act_values(p.act, acc);
+                        if (p.residual != nullptr) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) acc[j] += bf16_bits_to_float(res[j]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < nj) p.y[o0 + (size_t)j * ld] = float_to_bf16_bits(acc[j]);
+                }
+            }
+            if (!w.partial) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(cluster_map(&dempty[buf], 0));
+            }
+        }
+        if (!ok && lane == 0) fail();
+    }
+
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();  // no CTA leaves while the other may still use its memory
+    if (warp == 3) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+}  // namespace
+
+FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms) {
+    FfnPlan g{};
+    const int64_t tm = (M + 255) / 256;
+    g.bn = (int)(((M + tm - 1) / tm + 31) / 32 * 32);
+    g.pairs = std::max(1, num_sms / 2);
+    g.tiles_c = (rows + 255) / 256;
+    g.tiles = (int64_t)g.tiles_c * ((M + g.bn - 1) / g.bn);
+    const int rest = (int)(g.tiles % g.pairs);
+    // Cycles: a stage takes the longer of its MMAs and its dequant; joining a contributor's partial
+    // tile (512 bn bytes per CTA, written and read once) about 10 bn + 1500, and 3000 at the end.
+    const double stage = std::max(2.0 * g.bn, 240.0);
+    double best = 2.0 * entries * stage;
+    for (int n = 2; rest > 0 && n <= 16; ++n) {
+        const int runs = std::min(g.pairs, rest * n);
+        const int units = rest * entries;
+        if (units / runs < 2) break;
+        const double cost = 2.0 * stage * units / runs + (10.0 * g.bn + 1500.0) * n + 3000.0;
+        if (cost < best) {
+            best = cost;
+            g.cut = rest;
+            g.runs = runs;
+        }
+    }
+    g.partial_bytes = (size_t)(g.cut + g.runs) * 2 * 128 * g.bn * 4;
+    return g;
+}
+
+cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnArgs& a, bool back, bool two,
+                            float* partials, unsigned* counters, unsigned* err, cudaStream_t stream) {
+    GemmArgs2 g{};
+    g.w = a.w;
+    g.w2 = a.w2;
+    g.bias = a.bias;
+    g.residual = a.residual;
+    g.y = a.y;
+    g.pre = a.pre;
+    g.pre2 = a.pre2;
+    g.partials = partials;
+    g.counters = counters;
+    g.err = err;
+    g.M = (int)a.M;
+    g.N = a.N;
+    g.K = a.K;
+    g.gr = a.group_size / 128;
+    g.act = a.act;
+    g.bn = plan.bn;
+    g.entries1 = (back ? a.N : a.K) / 128;
+    g.entries = g.entries1 * (back && two ? 2 : 1);
+    g.tiles_c = plan.tiles_c;
+    g.tiles = (int)plan.tiles;
+    g.cut = plan.cut;
+    g.runs = plan.runs;
+    auto* fn = back ? ffn_gemm_kernel<kBackward> : two ? ffn_gemm_kernel<kGated> : ffn_gemm_kernel<kLinear>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const int64_t busy = plan.tiles > plan.cut ? std::max<int64_t>(plan.tiles - plan.cut, plan.runs) : plan.runs;
+    const int pairs = (int)std::min<int64_t>(plan.pairs, busy);
+    fn<<<2 * pairs, kThreads, kSmemBytes, stream>>>(maps.x, maps.x2, maps.w, maps.w2, g);
+    return cudaGetLastError();
+}
+
+}  // namespace w4a16

@@ -64,9 +64,15 @@
 //   - Programmatic dependent launch.  The weights may be fetched before the previous kernel
 //     on the stream has finished.  The helpers wait for it before they load x; the
 //     epilogue and the completion phase wait before they touch the workspace or y.
+//   - Epilogues (template parameter EPI).  kGemvPlain as above.  kGemvLinear adds bias, activation
+//     and residual to each row before its one rounding.  kGemvGated takes two weight matrices: a row
+//     block is 64 gate and 64 up rows, interleaved in eights (rows 16 i + 0..7 gate, + 8..15 up), so
+//     an m16 tile and every power-of-two share of a row block hold whole pairs; row r finds its
+//     partner in lane l ^ 8 when the sums are complete.
 #include <atomic>
 #include <mutex>
 
+#include "act.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -107,6 +113,17 @@ struct GemvArgs {
     int cl;              // 0: stream-K; else the cluster size of the cluster split-K (2..8, <= K/512)
     int ncl;             // cluster split-K: clusters (<= N/128); cluster j takes row blocks j, j + ncl, ...
     unsigned* err;
+    GemvEpilogue epi;    // kGemvLinear, kGemvGated
+};
+
+// The tensor maps a kernel instance takes.
+template <int EPI>
+struct GemvKernelMaps {
+    CUtensorMap w;
+};
+template <>
+struct GemvKernelMaps<kGemvGated> {
+    CUtensorMap w, w2;  // gate and up, boxes of 64 rows
 };
 
 template <int NT, int BITS = 4>
@@ -195,6 +212,58 @@ __device__ __forceinline__ void write_row(const GemvArgs& p, int n, const float 
         if (m < p.M) p.y[(size_t)m * p.N + n] = float_to_bf16_bits(v[m]);
 }
 
+// y of row r of row block rb, whose fp32 sums are v.  kGemvGated: the warp calls it as a whole (rows r of
+// its lanes, `in` where they belong to the caller), and row r's partner row sits in lane l ^ 8.
+template <int EPI>
+__device__ __forceinline__ void finish_row(const GemvArgs& p, int rb, int r, const float v[16], bool in = true) {
+    const int n = rb * kGemvRows + r;
+    if constexpr (EPI == kGemvPlain) {
+        if (in) write_row(p, n, v);
+    } else if constexpr (EPI == kGemvLinear) {
+        if (!in) return;
+        const GemvEpilogue& e = p.epi;
+        const float bias = e.bias != nullptr ? bf16_bits_to_float(e.bias[n]) : 0.0f;
+        float a[16];
+#pragma unroll
+        for (int m = 0; m < 16; ++m) a[m] = v[m] + bias;
+        if (e.pre != nullptr) {
+#pragma unroll
+            for (int m = 0; m < 16; ++m)
+                if (m < p.M) e.pre[(size_t)m * p.N + n] = float_to_bf16_bits(a[m]);
+        }
+        act_values(e.act, a);
+        if (e.residual != nullptr) {
+#pragma unroll
+            for (int m = 0; m < 16; ++m)
+                if (m < p.M) a[m] += bf16_bits_to_float(e.residual[(size_t)m * p.N + n]);
+        }
+#pragma unroll
+        for (int m = 0; m < 16; ++m)
+            if (m < p.M) p.y[(size_t)m * p.N + n] = float_to_bf16_bits(a[m]);
+    } else {
+        const GemvEpilogue& e = p.epi;
+        const bool up = (r & 8) != 0;
+        const int F = p.N >> 1, f = rb * (kGemvRows / 2) + 8 * (r >> 4) + (r & 7);
+        if (in && e.pre != nullptr) {
+            uint16_t* o = up ? e.pre2 : e.pre;
+#pragma unroll
+            for (int m = 0; m < 16; ++m)
+                if (m < p.M) o[(size_t)m * F + f] = float_to_bf16_bits(v[m]);
+        }
+        float g[16], u[16];
+#pragma unroll
+        for (int m = 0; m < 16; ++m) {
+            g[m] = v[m];
+            u[m] = __shfl_xor_sync(0xffffffffu, v[m], 8);  // in a gate lane: its up row
+        }
+        if (up || !in) return;
+        act_values(e.act, g);
+#pragma unroll
+        for (int m = 0; m < 16; ++m)
+            if (m < p.M) p.y[(size_t)m * F + f] = float_to_bf16_bits(g[m] * u[m]);
+    }
+}
+
 // Row block rb split between exactly two CTAs: when the other one has published its partial
 // tile (the counter, read with acquire semantics, is 1), loads that tile's rows lane + 32 i
 // into t[i] and returns true.  The calling CTA is then the row block's last contributor and
@@ -232,9 +301,21 @@ __device__ __forceinline__ bool gather_other(const GemvArgs& p, int rb, int GB, 
     return true;
 }
 
-template <int NT, int BITS>
+// One unit's packed weights into a stage: 128 rows of row block rb, 4 groups from gb.
+template <int EPI, int BITS>
+__device__ __forceinline__ void load_unit(uint8_t* dst, const GemvKernelMaps<EPI>& maps, uint64_t* bar, int rb, int gb) {
+    mbar_arrive_expect_tx(bar, (uint32_t)GemvW<BITS>::kWBytes);
+    if constexpr (EPI == kGemvGated) {
+        tma_load_3d(dst, &maps.w, bar, 0, rb * (kGemvRows / 2), gb * kGemvUnitGroups);
+        tma_load_3d(dst + GemvW<BITS>::kWBytes / 2, &maps.w2, bar, 0, rb * (kGemvRows / 2), gb * kGemvUnitGroups);
+    } else {
+        tma_load_3d(dst, &maps.w, bar, 0, rb * kGemvRows, gb * kGemvUnitGroups);
+    }
+}
+
+template <int NT, int BITS, int EPI>
 __global__ void __launch_bounds__(kGemvThreads, 1)
-gemv_w4a16_kernel(const __grid_constant__ CUtensorMap map_w, const GemvArgs p) {
+gemv_w4a16_kernel(const __grid_constant__ GemvKernelMaps<EPI> maps, const GemvArgs p) {
     using L = GemvSmem<NT, BITS>;
     constexpr int kWBytes = GemvW<BITS>::kWBytes;
     constexpr int S = kGemvStages;
@@ -291,14 +372,13 @@ gemv_w4a16_kernel(const __grid_constant__ CUtensorMap map_w, const GemvArgs p) {
     int pre = 0;                       // copies issued here (producer thread only)
     int prb = rb_first, pgb = gb_first;  // coordinates of the producer's next copy
     if (threadIdx.x == kGemvProducer * 32) {
-        prefetch_tensormap(&map_w);
+        prefetch_tensormap(&maps.w);
+        if constexpr (EPI == kGemvGated) prefetch_tensormap(&maps.w2);
         for (int i = 0; i < S; ++i) mbar_init(&wfull[i], 1u);
         fence_mbarrier_init();
         fence_proxy_async_smem();
-        for (; pre < S && pre < n; ++pre, walk_next(prb, pgb, kb, ke, step)) {
-            mbar_arrive_expect_tx(&wfull[pre], (uint32_t)kWBytes);
-            tma_load_3d(smem + pre * kWBytes, &map_w, &wfull[pre], 0, prb * kGemvRows, pgb * kGemvUnitGroups);
-        }
+        for (; pre < S && pre < n; ++pre, walk_next(prb, pgb, kb, ke, step))
+            load_unit<EPI, BITS>(smem + pre * kWBytes, maps, &wfull[pre], prb, pgb);
     }
     // the other barriers, one per thread, so that the prologue is short
     if (threadIdx.x >= S && threadIdx.x < 4 * S + 5) {
@@ -331,8 +411,7 @@ gemv_w4a16_kernel(const __grid_constant__ CUtensorMap map_w, const GemvArgs p) {
                     record_error(p.err, kErrTimeout);
                     break;
                 }
-                mbar_arrive_expect_tx(&wfull[slot], (uint32_t)kWBytes);
-                tma_load_3d(smem + slot * kWBytes, &map_w, &wfull[slot], 0, prb * kGemvRows, pgb * kGemvUnitGroups);
+                load_unit<EPI, BITS>(smem + slot * kWBytes, maps, &wfull[slot], prb, pgb);
                 ++issued;
             }
             // the copies this CTA started must land before it may exit
@@ -359,8 +438,15 @@ gemv_w4a16_kernel(const __grid_constant__ CUtensorMap map_w, const GemvArgs p) {
 #pragma unroll
             for (int gg = 0; gg < kGemvHG; ++gg) {
                 const int g = (gb * kGemvUnitGroups + kGemvHG * h + gg) / p.gr;  // the quantization group
-                scv[gg] = __ldg(reinterpret_cast<const uint2*>(p.scales + (size_t)g * p.N + (size_t)rb * kGemvRows) + lane);
-                zw[gg] = __ldg(p.zeros + (size_t)g * (p.N >> 3) + (size_t)rb * (kGemvRows / 8) + (lane >> 1));
+                if constexpr (EPI == kGemvGated) {  // rows 4 lane .. + 3: gate for lanes 0, 1 of every 4, else up
+                    const bool up = (lane & 2) != 0;
+                    const size_t c = (size_t)rb * (kGemvRows / 2) + 8 * (lane >> 2), F = (size_t)(p.N >> 1);
+                    scv[gg] = __ldg(reinterpret_cast<const uint2*>((up ? p.epi.scales2 : p.scales) + g * F + c) + (lane & 1));
+                    zw[gg] = __ldg((up ? p.epi.zeros2 : p.zeros) + g * (F >> 3) + (c >> 3));
+                } else {
+                    scv[gg] = __ldg(reinterpret_cast<const uint2*>(p.scales + (size_t)g * p.N + (size_t)rb * kGemvRows) + lane);
+                    zw[gg] = __ldg(p.zeros + (size_t)g * (p.N >> 3) + (size_t)rb * (kGemvRows / 8) + (lane >> 1));
+                }
             }
             if (s == 0) griddep_wait();  // x belongs to the stream order
 #pragma unroll
@@ -459,8 +545,14 @@ gemv_w4a16_kernel(const __grid_constant__ CUtensorMap map_w, const GemvArgs p) {
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
-                        const uint8_t* src = ws + (2 * half + gg) * GemvW<BITS>::kGroupBytes +
-                                             (rbase + 16 * i + 8 * hh) * GemvW<BITS>::kRowBytes;
+                        // gated: tile row halves hh 0 / 1 are the gate / up rows 16 (warp & 3) + 8 i + gq of
+                        // the stage's two boxes [4 groups][64 rows]
+                        const uint8_t* src =
+                            EPI == kGemvGated
+                                ? ws + hh * (kWBytes / 2) + (2 * half + gg) * (GemvW<BITS>::kGroupBytes / 2) +
+                                      (16 * (warp & 3) + 8 * i + gq) * GemvW<BITS>::kRowBytes
+                                : ws + (2 * half + gg) * GemvW<BITS>::kGroupBytes +
+                                      (rbase + 16 * i + 8 * hh) * GemvW<BITS>::kRowBytes;
                         if constexpr (BITS == 4) {
                             wv[gg][i][hh] = *reinterpret_cast<const uint4*>(src + 16 * t);
                         } else {  // the thread's 3 words of 32 codes
@@ -666,7 +758,7 @@ gemv_w4a16_kernel(const __grid_constant__ CUtensorMap map_w, const GemvArgs p) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int r = row0 + lane + 32 * i;
-                    if (r < row1) write_row(p, rb * kGemvRows + r, v[i]);
+                    finish_row<EPI>(p, rb, r, v[i], r < row1);
                 }
             } else if (lane == 0) {
                 record_error(p.err, kErrTimeout);
@@ -755,7 +847,7 @@ gemv_w4a16_kernel(const __grid_constant__ CUtensorMap map_w, const GemvArgs p) {
                             for (int e = 0; e < 4; ++e) v[c + e] = (0.0f + v[c + e]) + other[i][c + e];
                         }
                     }
-                    write_row(p, rb * kGemvRows + r, v);
+                    finish_row<EPI>(p, rb, r, v);
                 }
                 // the other contributor has arrived, so nothing else touches the counter
                 if (gathered && lane == 0) atomicExch(p.counters + rb, 0u);
@@ -816,7 +908,7 @@ gemv_w4a16_kernel(const __grid_constant__ CUtensorMap map_w, const GemvArgs p) {
                     }
                 }
             }
-            write_row(p, rb * kGemvRows + r, v);
+            finish_row<EPI>(p, rb, r, v);
         }
         asm volatile("bar.sync 2, %0;" ::"r"(32 * (kGemvConsumers + 1)) : "memory");
         if (threadIdx.x == 0)
@@ -870,9 +962,10 @@ int max_active_clusters(bool two, int cl) {
     std::atomic<int>& slot = cache[dev][two ? 1 : 0][cl];
     int v = slot.load(std::memory_order_relaxed);
     if (v >= 0) return v;
-    // the 4-bit kernel's figures; the 3-bit one needs less shared memory, so they hold for it too
+    // the plain 4-bit kernel's figures; the 3-bit one needs less shared memory and the other epilogues
+    // the same (one CTA per SM), so they hold for those too
     const int smem = two ? GemvSmem<2, 4>::kBytes : GemvSmem<1, 4>::kBytes;
-    const void* fn = two ? (const void*)gemv_w4a16_kernel<2, 4> : (const void*)gemv_w4a16_kernel<1, 4>;
+    const void* fn = two ? (const void*)gemv_w4a16_kernel<2, 4, kGemvPlain> : (const void*)gemv_w4a16_kernel<1, 4, kGemvPlain>;
     v = 0;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
@@ -896,7 +989,7 @@ int max_active_clusters(bool two, int cl) {
 
 }  // namespace
 
-GemvPlan gemv_plan(int M, int N, int K, int num_sms, int schedule) {
+GemvPlan gemv_plan(int M, int N, int K, int num_sms, int schedule, bool pairs) {
     const bool two = M > 8;
     const int NRB = N / kGemvRows, GB = K / (128 * kGemvUnitGroups);
     const long long T = (long long)NRB * GB;
@@ -908,6 +1001,7 @@ GemvPlan gemv_plan(int M, int N, int K, int num_sms, int schedule) {
     double cost_best = 0.0;
     if (schedule != W4A16_GEMV_STREAM_K) {
         for (int cl = 2; cl <= 8 && cl <= GB; ++cl) {
+            if (pairs && (cl & (cl - 1)) != 0) continue;  // a rank's rows must hold whole pairs of eights
             const int mac = max_active_clusters(two, cl);
             if (mac < 1) continue;
             const int ncl = NRB < mac ? NRB : mac;
@@ -927,11 +1021,12 @@ GemvPlan gemv_plan(int M, int N, int K, int num_sms, int schedule) {
     return best;
 }
 
-template <int NT, int BITS>
+template <int NT, int BITS, int EPI = kGemvPlain>
 static cudaError_t launch_gemv_kernel(const GemvMaps& maps, const GemvPlan& plan, const GemvArgs& a,
                                       cudaStream_t stream) {
     const int smem = GemvSmem<NT, BITS>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(gemv_w4a16_kernel<NT, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(gemv_w4a16_kernel<NT, BITS, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.P, 1, 1);
@@ -947,13 +1042,16 @@ static cudaError_t launch_gemv_kernel(const GemvMaps& maps, const GemvPlan& plan
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = plan.cluster != 0 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, gemv_w4a16_kernel<NT, BITS>, maps.w, a);
+    GemvKernelMaps<EPI> m;
+    m.w = maps.w;
+    if constexpr (EPI == kGemvGated) m.w2 = maps.w2;
+    return cudaLaunchKernelEx(&cfg, gemv_w4a16_kernel<NT, BITS, EPI>, m, a);
 }
 
 cudaError_t launch_gemv(const GemvMaps& maps, const GemvPlan& plan, int group_ratio, const uint16_t* x,
                         const uint16_t* scales, const uint32_t* zeros, const float* ysp, uint16_t* y,
                         float* partials, unsigned* counters, int M, int N, int K, unsigned* err,
-                        cudaStream_t stream, int bits) {
+                        cudaStream_t stream, int bits, const GemvEpilogue* epilogue) {
     GemvArgs a{};
     a.x = x;
     a.scales = scales;
@@ -974,6 +1072,15 @@ cudaError_t launch_gemv(const GemvMaps& maps, const GemvPlan& plan, int group_ra
     a.counters = counters;
 
     const bool two = M > 8;
+    if (epilogue != nullptr) {
+        if (bits != 4 || ysp != nullptr) return cudaErrorInvalidValue;
+        a.epi = *epilogue;
+        if (epilogue->kind == kGemvGated)
+            return two ? launch_gemv_kernel<2, 4, kGemvGated>(maps, plan, a, stream)
+                       : launch_gemv_kernel<1, 4, kGemvGated>(maps, plan, a, stream);
+        return two ? launch_gemv_kernel<2, 4, kGemvLinear>(maps, plan, a, stream)
+                   : launch_gemv_kernel<1, 4, kGemvLinear>(maps, plan, a, stream);
+    }
     if (bits == 3) return two ? launch_gemv_kernel<2, 3>(maps, plan, a, stream) : launch_gemv_kernel<1, 3>(maps, plan, a, stream);
     if (bits != 4) return cudaErrorInvalidValue;
     return two ? launch_gemv_kernel<2, 4>(maps, plan, a, stream) : launch_gemv_kernel<1, 4>(maps, plan, a, stream);

@@ -42,6 +42,20 @@ cudaError_t launch_gemv_nvfp4(const uint16_t* x, const uint32_t* qweight, const 
 // box 12 x 128 x 4: [4][128 rows][48 bytes].
 struct GemvMaps {
     CUtensorMap w;
+    CUtensorMap w2;  // gated: w and w2 are the gate and up weights, boxes 16 x 64 x 4
+};
+
+// What the GEMV does to its sums before the rounding to bf16.
+enum { kGemvPlain = 0, kGemvLinear = 1, kGemvGated = 2 };
+struct GemvEpilogue {
+    int kind;
+    int act;                  // w4a16_activation
+    const uint16_t* bias;     // kGemvLinear: [N], or nullptr
+    const uint16_t* residual; // kGemvLinear: [M][N], or nullptr
+    uint16_t* pre;            // the value before the activation (kGemvGated: g), or nullptr
+    uint16_t* pre2;           // kGemvGated: u, or nullptr
+    const uint16_t* scales2;  // kGemvGated: of the up weights
+    const uint32_t* zeros2;
 };
 
 // Largest K the GEMV supports.
@@ -69,16 +83,19 @@ struct GemvPlan {
 };
 
 // The launch for a schedule (W4A16_GEMV_AUTO, _STREAM_K or _CLUSTER) on the current device.
-GemvPlan gemv_plan(int M, int N, int K, int num_sms, int schedule);
+// pairs: the gated epilogue, whose clusters share a row block in powers of two.
+GemvPlan gemv_plan(int M, int N, int K, int num_sms, int schedule, bool pairs = false);
 
 // group_ratio: the quantization group size / 128 (1 for g128; K / 128 for one group per row).
 // ysp: nullptr, or the CSR term [N][M] fp32 written by launch_csr_rows just before (the GEMV
 // adds it to each output before rounding, after the previous kernel has finished).
 // bits: 4, or 3 for 3-bit codes (qweight [N][3K/32], the map's inner extent 12 words a group).
+// epilogue: nullptr for the plain product; with kGemvGated N counts both matrices' rows (2 F) and y
+// is [M][F].
 cudaError_t launch_gemv(const GemvMaps& maps, const GemvPlan& plan, int group_ratio, const uint16_t* x,
                         const uint16_t* scales, const uint32_t* zeros, const float* ysp, uint16_t* y,
                         float* partials, unsigned* counters, int M, int N, int K, unsigned* err,
-                        cudaStream_t stream, int bits = 4);
+                        cudaStream_t stream, int bits = 4, const GemvEpilogue* epilogue = nullptr);
 
 // The CSR term of the decode path: ysp[n][m] = sum_j float(val_j) * float(x[m][col_j]) over
 // row n's entries, in fp32 (see csr.cu).  1 <= M <= 16.  The next kernel on the stream may
@@ -165,7 +182,7 @@ struct PackedWeights {
     const uint32_t* zeros;
 };
 
-// A feed-forward product (see ffn.cu).  Forward: a = x [M][K], outputs [M][N].  Backward: a (and
+// A feed-forward product (see ffn_gemm.cu).  Forward: a = x [M][K], outputs [M][N].  Backward: a (and
 // a2) [M][N], output y [M][K].  w2, pre2 and a2 belong to the gated forms.
 struct FfnArgs {
     const uint16_t* a;
@@ -179,7 +196,27 @@ struct FfnArgs {
     int64_t M;
     int N, K, group_size, act;
 };
-cudaError_t launch_ffn(const FfnArgs& a, bool back, bool two, cudaStream_t stream);
+
+// The launch of a feed-forward product: rows = output channels (N, 2 F, or K backward), entries =
+// contraction / 128 over all weight matrices.
+struct FfnPlan {
+    int bn;          // tokens per tile
+    int pairs;       // CTA pairs of the device
+    int tiles_c;     // tiles along the output channels
+    int64_t tiles;
+    int cut, runs;   // tiles cut along the contraction, and the runs that they are cut into
+    size_t partial_bytes;
+};
+FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms);
+
+// Tensor maps: x, x2: the activations (dp, dp2 backward), boxes of 64 contraction steps x bn / 2 tokens,
+// 128-byte swizzle; w, w2: qweight [N][K/8], boxes of 16 words x 64 rows, 64-byte swizzle.
+struct FfnMaps {
+    CUtensorMap x, x2, w, w2;
+};
+// counters: 2 per cut tile, zero between calls.
+cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnArgs& a, bool back, bool two,
+                            float* partials, unsigned* counters, unsigned* err, cudaStream_t stream);
 
 // The elementwise steps of the backward passes.  sums: linear_dp_blocks(M) x N fp32, used with dbias.
 int linear_dp_blocks(int64_t M);
