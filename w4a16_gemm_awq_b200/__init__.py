@@ -512,9 +512,13 @@ def w4a16_fused_workspace_bytes(op: int, M: int, N: int, K: int) -> int:
     return int(lib().w4a16_fused_workspace_bytes(int(op), M, N, K))
 
 
+# These calls take 4 to 6 us inside the library, so the checks around them are kept to plain
+# attribute reads: one token's step is a chain of such calls.
+
 def _expect(t, dtype, shape, name, device):
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of shape {tuple(shape)} on {device}, got "
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        name = name if isinstance(name, str) else " ".join(name)
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
@@ -523,12 +527,13 @@ def _layer(w, K, group_size, name, device):
     qw, sc, z = w
     if qw.dim() != 2:
         raise ValueError(f"{name}: qweight must be a matrix")
-    N, gs = qw.shape[0], int(group_size)
-    if gs < 1 or K % gs != 0 or K % 8 != 0:
-        raise ValueError(f"{name}: group size {gs} does not divide K = {K}")
-    _expect(qw, torch.int32, (N, K // 8), f"{name} qweight", device)
-    _expect(sc, torch.int16, (K // gs, N), f"{name} scales", device)
-    _expect(z, torch.int32, (K // gs, N // 8), f"{name} zeros", device)
+    N = qw.shape[0]
+    if group_size < 1 or K % group_size != 0 or K % 8 != 0:
+        raise ValueError(f"{name}: group size {group_size} does not divide K = {K}")
+    G = K // group_size
+    _expect(qw, torch.int32, (N, K // 8), (name, "qweight"), device)
+    _expect(sc, torch.int16, (G, N), (name, "scales"), device)
+    _expect(z, torch.int32, (G, N // 8), (name, "zeros"), device)
     return Weights(qw.data_ptr(), sc.data_ptr(), z.data_ptr()), N
 
 
@@ -546,39 +551,22 @@ def _activation(a) -> int:
     return int(a)
 
 
-def _output(out, dtype, shape, name, device):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _expect(out, dtype, shape, name, device)
-    return out
-
-
 def _data(t):
     return t.data_ptr() if t is not None else None
 
 
-class _device_of:
-    """Makes a tensor's device the current one for a call, where it is not already."""
-
-    def __init__(self, device):
-        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 _fused_bytes = {}
 
 
-def _fused_workspace(ws, device, op, M, N, K):
-    """The caller's workspace, or the cached one of the current stream.  While the stream is being
-    captured, one of the graph's own, its counters zeroed by the graph: graphs share none, and a
-    later call that needs a larger one takes nothing from under a graph."""
+def _fused_workspace(ws, device, stream, op, M, N, K):
+    """(address, bytes) of the caller's workspace, or of the cached one of the current stream.  While
+    the stream is being captured: of one of the graph's own, its counters zeroed by the graph, so
+    that graphs share none and a later call that needs a larger one takes nothing from under a
+    graph."""
     if ws is not None:
         if ws.device != device or not ws.is_contiguous():
             raise ValueError(f"workspace: expected a contiguous tensor on {device}")
@@ -586,13 +574,21 @@ def _fused_workspace(ws, device, op, M, N, K):
     key = (device.index, op, M, N, K)
     nbytes = _fused_bytes.get(key)
     if nbytes is None:
-        nbytes = _fused_bytes[key] = w4a16_fused_workspace_bytes(op, M, N, K)
+        nbytes = w4a16_fused_workspace_bytes(op, M, N, K)
+        if len(_fused_bytes) < 65536:
+            _fused_bytes[key] = nbytes
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        ws = torch.empty(max(nbytes, _WORKSPACE_ZERO_BYTES), dtype=torch.uint8, device=device)
         ws[:_WORKSPACE_ZERO_BYTES].zero_()
     else:
-        ws = workspace(device, nbytes)
+        ws = _workspaces.get((device.index, stream))
+        if ws is None or ws.numel() < nbytes:
+            ws = workspace(device, nbytes)
     return ws.data_ptr(), ws.numel()
+
+
+def _elsewhere(device):
+    return device.index != torch.cuda.current_device()
 
 
 def w4a16_linear_fused(x, qweight, scales, zeros, bias=None, residual=None, activation="none", group_size=128,
@@ -602,6 +598,10 @@ def w4a16_linear_fused(x, qweight, scales, zeros, bias=None, residual=None, acti
     before the activation (for the backward pass)."""
     M, K = _rows(x, "x")
     dev = x.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return w4a16_linear_fused(x, qweight, scales, zeros, bias, residual, activation, group_size, out, pre_out,
+                                      workspace)
     w, N = _layer((qweight, scales, zeros), K, group_size, "weights", dev)
     if bias is not None:
         _expect(bias, torch.bfloat16, (N,), "bias", dev)
@@ -609,13 +609,15 @@ def w4a16_linear_fused(x, qweight, scales, zeros, bias=None, residual=None, acti
         _expect(residual, torch.bfloat16, (M, N), "residual", dev)
     if pre_out is not None:
         _expect(pre_out, torch.bfloat16, (M, N), "pre_out", dev)
-    act = _activation(activation)
-    with _device_of(dev):
-        y = _output(out, torch.bfloat16, (M, N), "out", dev)
-        ws, wsb = _fused_workspace(workspace, dev, OP_LINEAR, M, N, K)
-        _check(lib().w4a16_linear_fused(x.data_ptr(), w, _data(bias), _data(residual), y.data_ptr(), _data(pre_out),
-                                        M, N, K, int(group_size), act, ws, wsb, _stream(dev)), "w4a16_linear_fused")
-    return y
+    if out is None:
+        out = x.new_empty((M, N))
+    else:
+        _expect(out, torch.bfloat16, (M, N), "out", dev)
+    stream = _raw_stream(dev)
+    ws, wsb = _fused_workspace(workspace, dev, stream, OP_LINEAR, M, N, K)
+    _check(lib().w4a16_linear_fused(x.data_ptr(), w, _data(bias), _data(residual), out.data_ptr(), _data(pre_out), M, N,
+                                    K, group_size, _activation(activation), ws, wsb, stream), "w4a16_linear_fused")
+    return out
 
 
 def w4a16_linear_fused_backward(dy, qweight, scales, zeros, pre=None, activation="none", group_size=128,
@@ -625,6 +627,10 @@ def w4a16_linear_fused_backward(dy, qweight, scales, zeros, pre=None, activation
     residual's gradient."""
     M, N = _rows(dy, "dy")
     dev = dy.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return w4a16_linear_fused_backward(dy, qweight, scales, zeros, pre, activation, group_size, bias_grad, out,
+                                               workspace)
     if qweight.dim() != 2 or qweight.shape[0] != N:
         raise ValueError(f"qweight {tuple(qweight.shape)} does not match dy {tuple(dy.shape)}")
     K = qweight.shape[1] * 8
@@ -634,14 +640,16 @@ def w4a16_linear_fused_backward(dy, qweight, scales, zeros, pre=None, activation
         raise ValueError("pre: needed for the gradient of an activation")
     if pre is not None:
         _expect(pre, torch.bfloat16, (M, N), "pre", dev)
-    with _device_of(dev):
-        dx = _output(out, torch.bfloat16, (M, K), "out", dev)
-        db = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
-        ws, wsb = _fused_workspace(workspace, dev, OP_LINEAR_BACKWARD, M, N, K)
-        _check(lib().w4a16_linear_fused_backward(dy.data_ptr(), _data(pre), w, dx.data_ptr(), _data(db), M, N, K,
-                                                 int(group_size), act, ws, wsb, _stream(dev)),
-               "w4a16_linear_fused_backward")
-    return dx, db
+    if out is None:
+        out = dy.new_empty((M, K))
+    else:
+        _expect(out, torch.bfloat16, (M, K), "out", dev)
+    db = dy.new_empty(N, dtype=torch.float32) if bias_grad else None
+    stream = _raw_stream(dev)
+    ws, wsb = _fused_workspace(workspace, dev, stream, OP_LINEAR_BACKWARD, M, N, K)
+    _check(lib().w4a16_linear_fused_backward(dy.data_ptr(), _data(pre), w, out.data_ptr(), _data(db), M, N, K,
+                                             group_size, act, ws, wsb, stream), "w4a16_linear_fused_backward")
+    return out, db
 
 
 def w4a16_gated(x, gate, up, activation="silu", group_size=128, out=None, save=False, workspace=None):
@@ -650,25 +658,32 @@ def w4a16_gated(x, gate, up, activation="silu", group_size=128, out=None, save=F
     in bf16 for the backward pass."""
     M, K = _rows(x, "x")
     dev = x.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return w4a16_gated(x, gate, up, activation, group_size, out, save, workspace)
     wg, F = _layer(gate, K, group_size, "gate", dev)
     wu, Fu = _layer(up, K, group_size, "up", dev)
     if F != Fu:
         raise ValueError(f"gate has {F} output channels, up has {Fu}")
-    act = _activation(activation)
-    with _device_of(dev):
-        h = _output(out, torch.bfloat16, (M, F), "out", dev)
-        g = torch.empty(M, F, dtype=torch.bfloat16, device=dev) if save else None
-        u = torch.empty(M, F, dtype=torch.bfloat16, device=dev) if save else None
-        ws, wsb = _fused_workspace(workspace, dev, OP_GATED, M, F, K)
-        _check(lib().w4a16_gated(x.data_ptr(), wg, wu, h.data_ptr(), _data(g), _data(u), M, F, K, int(group_size), act,
-                                 ws, wsb, _stream(dev)), "w4a16_gated")
-    return (h, g, u) if save else h
+    if out is None:
+        out = x.new_empty((M, F))
+    else:
+        _expect(out, torch.bfloat16, (M, F), "out", dev)
+    g, u = (torch.empty_like(out), torch.empty_like(out)) if save else (None, None)
+    stream = _raw_stream(dev)
+    ws, wsb = _fused_workspace(workspace, dev, stream, OP_GATED, M, F, K)
+    _check(lib().w4a16_gated(x.data_ptr(), wg, wu, out.data_ptr(), _data(g), _data(u), M, F, K, group_size,
+                             _activation(activation), ws, wsb, stream), "w4a16_gated")
+    return (out, g, u) if save else out
 
 
 def w4a16_gated_backward(dh, g, u, gate, up, activation="silu", group_size=128, out=None, workspace=None):
     """dx bf16 [M][K] of w4a16_gated from dh bf16 [M][F] and the g, u that it saved."""
     M, F = _rows(dh, "dh")
     dev = dh.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return w4a16_gated_backward(dh, g, u, gate, up, activation, group_size, out, workspace)
     _expect(g, torch.bfloat16, (M, F), "g", dev)
     _expect(u, torch.bfloat16, (M, F), "u", dev)
     K = gate[0].shape[-1] * 8
@@ -676,69 +691,98 @@ def w4a16_gated_backward(dh, g, u, gate, up, activation="silu", group_size=128, 
     wu, Fu = _layer(up, K, group_size, "up", dev)
     if Fg != F or Fu != F:
         raise ValueError(f"gate and up have {Fg} and {Fu} output channels, dh has {F}")
-    act = _activation(activation)
-    with _device_of(dev):
-        dx = _output(out, torch.bfloat16, (M, K), "out", dev)
-        ws, wsb = _fused_workspace(workspace, dev, OP_GATED_BACKWARD, M, F, K)
-        _check(lib().w4a16_gated_backward(dh.data_ptr(), g.data_ptr(), u.data_ptr(), wg, wu, dx.data_ptr(), M, F, K,
-                                          int(group_size), act, ws, wsb, _stream(dev)), "w4a16_gated_backward")
-    return dx
+    if out is None:
+        out = dh.new_empty((M, K))
+    else:
+        _expect(out, torch.bfloat16, (M, K), "out", dev)
+    stream = _raw_stream(dev)
+    ws, wsb = _fused_workspace(workspace, dev, stream, OP_GATED_BACKWARD, M, F, K)
+    _check(lib().w4a16_gated_backward(dh.data_ptr(), g.data_ptr(), u.data_ptr(), wg, wu, out.data_ptr(), M, F, K,
+                                      group_size, _activation(activation), ws, wsb, stream), "w4a16_gated_backward")
+    return out
 
 
-def _norm_operands(x, weight, residual, s):
-    M, K = _rows(x, "x")
+def _norm_operands(x, name, weight, s):
+    M, K = _rows(x, name)
     _expect(weight, torch.bfloat16, (K,), "weight", x.device)
-    if residual is not None:
-        _expect(residual, torch.bfloat16, (M, K), "residual", x.device)
     if s is not None:
         _expect(s, torch.float32, (K,), "s", x.device)
     return M, K, x.device
+
+
+def _sum_output(x, residual, sum_out, M, K, dev):
+    """Where the sum h goes: None without a residual, unless the caller wants it written."""
+    if residual is not None:
+        _expect(residual, torch.bfloat16, (M, K), "residual", dev)
+    if sum_out is not None:
+        _expect(sum_out, torch.bfloat16, (M, K), "sum_out", dev)
+        return sum_out
+    return torch.empty_like(x) if residual is not None else None
 
 
 def awq_rmsnorm(x, weight, residual=None, s=None, eps=1e-6, out=None, sum_out=None):
     """(y, h): h = bf16(x + residual), written to sum_out (a new tensor by default; x or residual for
     the addition in place), and y = bf16(h * rsqrt(mean h^2 + eps) * weight / s).  Without a
     residual h is x itself, unless sum_out is given."""
-    M, K, dev = _norm_operands(x, weight, residual, s)
-    with _device_of(dev):
-        y = _output(out, torch.bfloat16, (M, K), "out", dev)
-        h = None if residual is None and sum_out is None else _output(sum_out, torch.bfloat16, (M, K), "sum_out", dev)
-        _check(lib().awq_rmsnorm(x.data_ptr(), _data(residual), weight.data_ptr(), _data(s), eps, _data(h),
-                                 y.data_ptr(), M, K, _stream(dev)), "awq_rmsnorm")
-    return y, x if h is None else h
+    M, K, dev = _norm_operands(x, "x", weight, s)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return awq_rmsnorm(x, weight, residual, s, eps, out, sum_out)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _expect(out, torch.bfloat16, (M, K), "out", dev)
+    h = _sum_output(x, residual, sum_out, M, K, dev)
+    _check(lib().awq_rmsnorm(x.data_ptr(), _data(residual), weight.data_ptr(), _data(s), eps, _data(h), out.data_ptr(),
+                             M, K, _raw_stream(dev)), "awq_rmsnorm")
+    return out, x if h is None else h
 
 
 def awq_rmsnorm_e4m3(x, weight, residual=None, s=None, eps=1e-6, group_size=0, out=None, scales_out=None, sum_out=None):
     """(q, scales, h): awq_rmsnorm with its output in 8 bits: q float8_e4m3fn [M][K] and scales fp32
     [M][K/group_size], the output being about q * scale.  group_size 0: one scale per row."""
-    M, K, dev = _norm_operands(x, weight, residual, s)
+    M, K, dev = _norm_operands(x, "x", weight, s)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return awq_rmsnorm_e4m3(x, weight, residual, s, eps, group_size, out, scales_out, sum_out)
     gs = int(group_size) or K
     if gs < 1 or K % gs != 0:
         raise ValueError(f"group size {gs} does not divide K = {K}")
-    with _device_of(dev):
-        q = _output(out, torch.float8_e4m3fn, (M, K), "out", dev)
-        sc = _output(scales_out, torch.float32, (M, K // gs), "scales_out", dev)
-        h = None if residual is None and sum_out is None else _output(sum_out, torch.bfloat16, (M, K), "sum_out", dev)
-        _check(lib().awq_rmsnorm_e4m3(x.data_ptr(), _data(residual), weight.data_ptr(), _data(s), eps, _data(h),
-                                      q.data_ptr(), sc.data_ptr(), M, K, gs, _stream(dev)), "awq_rmsnorm_e4m3")
-    return q, sc, x if h is None else h
+    if out is None:
+        out = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    else:
+        _expect(out, torch.float8_e4m3fn, (M, K), "out", dev)
+    if scales_out is None:
+        scales_out = x.new_empty((M, K // gs), dtype=torch.float32)
+    else:
+        _expect(scales_out, torch.float32, (M, K // gs), "scales_out", dev)
+    h = _sum_output(x, residual, sum_out, M, K, dev)
+    _check(lib().awq_rmsnorm_e4m3(x.data_ptr(), _data(residual), weight.data_ptr(), _data(s), eps, _data(h),
+                                  out.data_ptr(), scales_out.data_ptr(), M, K, gs, _raw_stream(dev)), "awq_rmsnorm_e4m3")
+    return out, scales_out, x if h is None else h
 
 
 def awq_rmsnorm_backward(dy, h, weight, s=None, dh=None, eps=1e-6, weight_grad=True, out=None, workspace=None):
     """(dx bf16 [M][K], dweight fp32 [K] or None) of awq_rmsnorm at the sum h; dh, if given, is the
     gradient that reaches h along the residual stream.  dx is the gradient of x and of residual."""
-    M, K, dev = _norm_operands(dy, weight, h, s)
+    M, K, dev = _norm_operands(dy, "dy", weight, s)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return awq_rmsnorm_backward(dy, h, weight, s, dh, eps, weight_grad, out, workspace)
+    _expect(h, torch.bfloat16, (M, K), "h", dev)
     if dh is not None:
         _expect(dh, torch.bfloat16, (M, K), "dh", dev)
-    with _device_of(dev):
-        dx = _output(out, torch.bfloat16, (M, K), "out", dev)
-        dw, ws, wsb = None, None, 0
-        if weight_grad:
-            dw = torch.empty(K, dtype=torch.float32, device=dev)
-            ws, wsb = _fused_workspace(workspace, dev, OP_RMSNORM_BACKWARD, M, 0, K)
-        _check(lib().awq_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _data(s), _data(dh), eps,
-                                          dx.data_ptr(), _data(dw), M, K, ws, wsb, _stream(dev)), "awq_rmsnorm_backward")
-    return dx, dw
+    if out is None:
+        out = torch.empty_like(dy)
+    else:
+        _expect(out, torch.bfloat16, (M, K), "out", dev)
+    dw, ws, wsb, stream = None, None, 0, _raw_stream(dev)
+    if weight_grad:
+        dw = dy.new_empty(K, dtype=torch.float32)
+        ws, wsb = _fused_workspace(workspace, dev, stream, OP_RMSNORM_BACKWARD, M, 0, K)
+    _check(lib().awq_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _data(s), _data(dh), eps,
+                                      out.data_ptr(), _data(dw), M, K, ws, wsb, stream), "awq_rmsnorm_backward")
+    return out, dw
 
 
 w4a16_workspace_bytes = workspace_bytes

@@ -920,7 +920,8 @@ w4a16_status w4a16_linear_fused_backward(const uint16_t* dy, const uint16_t* pre
     uint16_t* dp = act ? reinterpret_cast<uint16_t*>(grads) : nullptr;
     float* sums = reinterpret_cast<float*>(grads + backward_dp_bytes(M, N));
     if (act || dbias) {
-        st = from_cuda(launch_linear_dp(dy, pre, dp, dbias, sums, M, (int)N, activation, s));
+        st = from_cuda(launch_linear_dp(dy, pre, dp, dbias, sums, static_cast<unsigned*>(workspace), M, (int)N, activation,
+                                        s));
         if (st != W4A16_OK) return st;
     }
     a.a = act ? dp : dy;

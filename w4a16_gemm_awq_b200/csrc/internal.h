@@ -220,8 +220,9 @@ cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnA
 
 // The elementwise steps of the backward passes.  sums: linear_dp_blocks(M) x N fp32, used with dbias.
 int linear_dp_blocks(int64_t M);
+// counters: one per 256 columns, zero between calls.
 cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* dbias, float* sums,
-                             int64_t M, int N, int act, cudaStream_t stream);
+                             unsigned* counters, int64_t M, int N, int act, cudaStream_t stream);
 cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dg, uint16_t* du,
                             int64_t M, int F, int act, int num_sms, cudaStream_t stream);
 
