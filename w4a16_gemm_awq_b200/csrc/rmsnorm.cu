@@ -6,8 +6,12 @@
 //   backward: xhat = h rstd;  w = dy weight / s;  dx = dh + rstd (w - xhat mean(w xhat));
 //             dweight = sum over rows of dy xhat / s
 //
-// One block per row at a time, the row in registers (8 channels per thread and chunk), so every
-// input is read once and every output written once: memory bound.  Sums are fp32.
+// Memory bound: a row sits in registers (8 channels per thread and chunk), so every input is read
+// once and every output written once; sums are fp32.  Many rows: 4 chunks per thread, so that a block
+// has up to 8 independent 16-byte loads per thread in flight and several rows share an SM; each block
+// walks rows and keeps weight / s in registers.  Few rows: as many threads per row as it has chunks,
+// which shortens the one row's latency.  The backward pass runs several rows per block side by side
+// (one group of warps each, with its own barrier) so that few partial sums of dweight are left.
 #include "common.cuh"
 #include "internal.h"
 
@@ -80,16 +84,22 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum over the block in a fixed order.  buf: 32 floats; two buffers used in turn need no second
-// barrier.
-__device__ __forceinline__ float block_sum(float v, float* buf) {
-    v = warp_sum(v);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    const int l = threadIdx.x & 31;
-    return warp_sum(l < warps ? buf[l] : 0.0f);
+// Sums of N values over a group of `threads` threads (whole warps) in a fixed order.  buf: [N][32]
+// floats; two buffers used in turn need no second barrier.  bar: the group's barrier.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float (*buf)[32], int t, int threads, int bar) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    const int warps = threads >> 5;
+    if (warps == 1) return;
+    if ((t & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) buf[i][t >> 5] = v[i];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+    const int l = t & 31;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(l < warps ? buf[i][l] : 0.0f);
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -98,131 +108,199 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// V: chunks of 8 channels per thread.  Q8: the e4m3 output.
-template <int V, bool Q8>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs p) {
-    __shared__ float buf[2][32];
-    __shared__ uint32_t amax[Q8 ? 256 : 1];  // per group of a row, as bits of |v|: NaN > inf > finite
-    const int T = blockDim.x, K = p.K;
-    float ws[V][8];
+// V: chunks of 8 channels per thread.  MAXT: most threads.  Q8: the e4m3 output.
+template <int V, int MAXT, bool Q8>
+__global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const NormArgs p) {
+    constexpr bool kKeep = V * MAXT <= 2048;  // weight / s stay in registers
+    __shared__ float buf[2][1][32];
+    __shared__ uint32_t amax[2][Q8 ? 256 : 1];  // per group of a row, as bits of |v|: NaN > inf > finite
+    const int T = blockDim.x, t = threadIdx.x, K = p.K;
+    float ws[kKeep ? V : 1][8];
+    if constexpr (kKeep) {
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-        const int k = (c * T + threadIdx.x) * 8;
-        if (k < K) load_ws(p.weight, p.s, k, ws[c]);
+        for (int c = 0; c < V; ++c) {
+            const int k = (c * T + t) * 8;
+            if (k < K) load_ws(p.weight, p.s, k, ws[c]);
+        }
+    }
+    const int groups = Q8 ? K / p.group : 0;
+    const bool shared_max = Q8 && p.group != 128;  // a group of 128 is 16 lanes of one warp
+    if (shared_max) {
+        for (int i = t; i < groups; i += T) amax[0][i] = 0u;
+        __syncthreads();
     }
     int flip = 0;
     for (long long m = blockIdx.x; m < p.M; m += gridDim.x, flip ^= 1) {
-        float f[V][8];
-        float ss = 0.0f;
-        if constexpr (Q8) {
-            __syncthreads();  // the previous row's maxima have been read
-            for (int i = threadIdx.x; i < K / p.group; i += T) amax[i] = 0u;
-        }
+        const size_t row = (size_t)m * K;
+        uint4 a[V], r[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            const int k = (c * T + threadIdx.x) * 8;
+            const int k = (c * T + t) * 8;
             if (k < K) {
-                uint4 a = *reinterpret_cast<const uint4*>(p.x + m * K + k);
-                unpack8(a, f[c]);
+                a[c] = __ldcs(reinterpret_cast<const uint4*>(p.x + row + k));
+                if (p.residual != nullptr) r[c] = __ldcs(reinterpret_cast<const uint4*>(p.residual + row + k));
+            }
+        }
+        // the row as rounded to bf16 stays packed in a: h is exact there, and the norm is that of h
+        float ss[1] = {0.0f};
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int k = (c * T + t) * 8;
+            if (k < K) {
+                float f[8];
+                unpack8(a[c], f);
                 if (p.residual != nullptr) {
-                    float r[8];
-                    unpack8(*reinterpret_cast<const uint4*>(p.residual + m * K + k), r);
+                    float g[8];
+                    unpack8(r[c], g);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[c][e] += r[e];
-                    a = pack8(f[c]);
-                    unpack8(a, f[c]);  // the norm is that of the rounded sum
+                    for (int e = 0; e < 8; ++e) f[e] += g[e];
+                    a[c] = pack8(f);
+                    unpack8(a[c], f);
                 }
-                if (p.h != nullptr) *reinterpret_cast<uint4*>(p.h + m * K + k) = a;
+                if (p.h != nullptr) *reinterpret_cast<uint4*>(p.h + row + k) = a[c];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(f[c][e], f[c][e], ss);
+                for (int e = 0; e < 8; ++e) ss[0] = fmaf(f[e], f[e], ss[0]);
             }
         }
-        const float rstd = rsqrtf(block_sum(ss, buf[flip]) / (float)K + p.eps);
+        group_sum<1>(ss, buf[flip], t, T, 1);
+        const float rstd = rsqrtf(ss[0] / (float)K + p.eps);
+        auto scaled = [&](int c, int k, float f[8]) {  // v of chunk c
+            float w[8];
+            if constexpr (kKeep) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = ws[c][e];
+            } else {
+                load_ws(p.weight, p.s, k, w);
+            }
+            unpack8(a[c], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * w[e];
+        };
+        uint32_t lane_max[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            const int k = (c * T + threadIdx.x) * 8;
+            const int k = (c * T + t) * 8;
+            lane_max[c] = 0u;
             if (k < K) {
+                float f[8];
+                scaled(c, k, f);
+                if constexpr (Q8) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[c][e] = f[c][e] * rstd * ws[c][e];
-                if constexpr (!Q8) *reinterpret_cast<uint4*>(p.y + m * K + k) = pack8(f[c]);
+                    for (int e = 0; e < 8; ++e) lane_max[c] = max(lane_max[c], __float_as_uint(f[e]) & 0x7FFFFFFFu);
+                } else {
+                    *reinterpret_cast<uint4*>(p.y + row + k) = pack8(f);
+                }
             }
         }
         if constexpr (Q8) {
-            if ((T >> 5) == 1) __syncthreads();  // block_sum had no barrier after amax was cleared
 #pragma unroll
             for (int c = 0; c < V; ++c) {
-                const int k = (c * T + threadIdx.x) * 8;
-                uint32_t a = 0;
-                if (k < K) {
+                // 16 lanes hold 128 channels, all of one group
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(f[c][e]) & 0x7FFFFFFFu);
-                    atomicMax(&amax[k / p.group], a);
-                }
+                for (int o = 8; o > 0; o >>= 1) lane_max[c] = max(lane_max[c], __shfl_xor_sync(0xffffffffu, lane_max[c], o));
+                const int k = (c * T + t) * 8;
+                if (shared_max && (t & 15) == 0 && k < K) atomicMax(&amax[flip][k / p.group], lane_max[c]);
             }
-            __syncthreads();
+            if (shared_max) {
+                __syncthreads();
+                // the other buffer: read last in the previous row, used next in the next one
+                for (int i = t; i < groups; i += T) amax[flip ^ 1][i] = 0u;
+            }
 #pragma unroll
             for (int c = 0; c < V; ++c) {
-                const int k = (c * T + threadIdx.x) * 8;
+                const int k = (c * T + t) * 8;
                 if (k < K) {
-                    const float am = __uint_as_float(amax[k / p.group]);
+                    const int g = k / p.group;
+                    const float am = __uint_as_float(shared_max ? amax[flip][g] : lane_max[c]);
                     const float sc = (am < kTiny ? kTiny : am) / kE4m3Max;
+                    const float inv = 1.0f / sc;
+                    float f[8];
+                    scaled(c, k, f);
                     uint32_t w[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        w[i] = e4m3x2(f[c][4 * i] / sc, f[c][4 * i + 1] / sc) |
-                               (e4m3x2(f[c][4 * i + 2] / sc, f[c][4 * i + 3] / sc) << 16);
-                    *reinterpret_cast<uint2*>(p.q + m * K + k) = make_uint2(w[0], w[1]);
-                    if (k % p.group == 0) p.scales[m * (K / p.group) + k / p.group] = sc;
+                        w[i] = e4m3x2(f[4 * i] * inv, f[4 * i + 1] * inv) |
+                               (e4m3x2(f[4 * i + 2] * inv, f[4 * i + 3] * inv) << 16);
+                    *reinterpret_cast<uint2*>(p.q + row + k) = make_uint2(w[0], w[1]);
+                    if (k % p.group == 0) p.scales[(size_t)m * groups + g] = sc;
                 }
             }
+            if (shared_max) __syncthreads();  // the cleared maxima are seen before the next row's
         }
     }
 }
 
-template <int V>
-__global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBwdArgs p) {
-    __shared__ float buf[2][2][32];
-    const int T = blockDim.x, K = p.K;
-    float dw[V][8];
+// A block holds blockDim.x / T groups of T threads, each on a row of its own.
+template <int V, int MAXT>
+__global__ void __launch_bounds__(MAXT) rmsnorm_backward_kernel(const NormBwdArgs p, int T) {
+    constexpr bool kKeep = V * MAXT <= 2048;
+    constexpr int kGroups = 8;
+    __shared__ float buf[kGroups][2][2][32];
+    extern __shared__ float4 part[];  // [groups - 1][K] sums of the other groups, when there are several
+    const int K = p.K, grp = threadIdx.x / T, t = threadIdx.x - grp * T, groups = blockDim.x / T;
+    float dw[V][8], ws[kKeep ? V : 1][8];
 #pragma unroll
-    for (int c = 0; c < V; ++c)
+    for (int c = 0; c < V; ++c) {
+        const int k = (c * T + t) * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[c][e] = 0.0f;
+        if constexpr (kKeep) {
+            if (k < K) load_ws(p.weight, p.s, k, ws[c]);
+        }
+    }
     int flip = 0;
-    for (long long m = blockIdx.x; m < p.M; m += gridDim.x, flip ^= 1) {
-        uint4 g[V], hv[V];
-        float ss = 0.0f, sv = 0.0f;
+    const long long step = (long long)gridDim.x * groups;
+    for (long long m = (long long)blockIdx.x * groups + grp; m < p.M; m += step, flip ^= 1) {
+        const size_t row = (size_t)m * K;
+        uint4 g[V], hv[V], d4[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            const int k = (c * T + threadIdx.x) * 8;
+            const int k = (c * T + t) * 8;
             if (k < K) {
-                g[c] = *reinterpret_cast<const uint4*>(p.dy + m * K + k);
-                hv[c] = *reinterpret_cast<const uint4*>(p.h + m * K + k);
-                float a[8], h[8], ws[8];
+                g[c] = __ldcs(reinterpret_cast<const uint4*>(p.dy + row + k));
+                hv[c] = __ldcs(reinterpret_cast<const uint4*>(p.h + row + k));
+                if (p.dh != nullptr) d4[c] = __ldcs(reinterpret_cast<const uint4*>(p.dh + row + k));
+            }
+        }
+        float s[2] = {0.0f, 0.0f};  // h^2, v h
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int k = (c * T + t) * 8;
+            if (k < K) {
+                float a[8], h[8], w[8];
                 unpack8(g[c], a);
                 unpack8(hv[c], h);
-                load_ws(p.weight, p.s, k, ws);
+                if constexpr (kKeep) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = ws[c][e];
+                } else {
+                    load_ws(p.weight, p.s, k, w);
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    ss = fmaf(h[e], h[e], ss);
-                    sv = fmaf(a[e] * ws[e], h[e], sv);
+                    s[0] = fmaf(h[e], h[e], s[0]);
+                    s[1] = fmaf(a[e] * w[e], h[e], s[1]);
                 }
             }
         }
-        ss = block_sum(ss, buf[flip][0]);
-        sv = block_sum(sv, buf[flip][1]);
-        const float rstd = rsqrtf(ss / (float)K + p.eps);
-        const float mean = sv * rstd / (float)K;  // mean of v xhat
+        group_sum<2>(s, buf[grp][flip], t, T, 1 + grp);
+        const float rstd = rsqrtf(s[0] / (float)K + p.eps);
+        const float mean = s[1] * rstd / (float)K;  // mean of v xhat
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            const int k = (c * T + threadIdx.x) * 8;
+            const int k = (c * T + t) * 8;
             if (k < K) {
-                float a[8], h[8], ws[8], d[8];
+                float a[8], h[8], w[8], d[8];
                 unpack8(g[c], a);
                 unpack8(hv[c], h);
-                load_ws(p.weight, p.s, k, ws);
+                if constexpr (kKeep) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = ws[c][e];
+                } else {
+                    load_ws(p.weight, p.s, k, w);
+                }
                 if (p.dh != nullptr) {
-                    unpack8(*reinterpret_cast<const uint4*>(p.dh + m * K + k), d);
+                    unpack8(d4[c], d);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) d[e] = 0.0f;
@@ -231,66 +309,111 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBwdArg
                 for (int e = 0; e < 8; ++e) {
                     const float xh = h[e] * rstd;
                     dw[c][e] = fmaf(a[e], xh, dw[c][e]);
-                    d[e] = fmaf(rstd, a[e] * ws[e] - xh * mean, d[e]);
+                    d[e] = fmaf(rstd, a[e] * w[e] - xh * mean, d[e]);
                 }
-                *reinterpret_cast<uint4*>(p.dx + m * K + k) = pack8(d);
+                *reinterpret_cast<uint4*>(p.dx + row + k) = pack8(d);
             }
         }
     }
-    if (p.partials != nullptr) {
+    if (p.partials == nullptr) return;
+    // the groups' sums in group order, then one row of partials per block
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-            const int k = (c * T + threadIdx.x) * 8;
-            if (k < K) {
-                float4* dst = reinterpret_cast<float4*>(p.partials + (size_t)blockIdx.x * K + k);
-                dst[0] = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
-                dst[1] = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
+    for (int c = 0; c < V; ++c) {
+        const int k = (c * T + t) * 8;
+        if (k < K && grp > 0) {
+            float4* dst = part + ((size_t)(grp - 1) * K + k) / 4;
+            dst[0] = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
+            dst[1] = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
+        }
+    }
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+        const int k = (c * T + t) * 8;
+        if (k < K) {
+            float4 a = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
+            float4 b = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
+            for (int q = 0; q < groups - 1; ++q) {
+                const float4* src = part + ((size_t)q * K + k) / 4;
+                a.x += src[0].x; a.y += src[0].y; a.z += src[0].z; a.w += src[0].w;
+                b.x += src[1].x; b.y += src[1].y; b.z += src[1].z; b.w += src[1].w;
             }
+            float4* dst = reinterpret_cast<float4*>(p.partials + (size_t)blockIdx.x * K + k);
+            dst[0] = a;
+            dst[1] = b;
         }
     }
 }
 
-// dweight[k] = (sum over rows of partials[r][k], in row order) / s[k]
+// dweight[k] = (sum over the R rows of partials) / s[k]: 32 columns per block, 8 row strides side by
+// side, joined in a fixed order.
 __global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* partials, const float* s, float* dweight,
                                                               int R, int K) {
-    const int k = blockIdx.x * 256 + threadIdx.x;
-    if (k >= K) return;
+    __shared__ float part[8][32];
+    const int lane = threadIdx.x & 31, rt = threadIdx.x >> 5;
+    const int k = blockIdx.x * 32 + lane;
     float a = 0.0f;
-    for (int r = 0; r < R; ++r) a += partials[(size_t)r * K + k];
+    if (k < K) {
+#pragma unroll 8
+        for (int r = rt; r < R; r += 8) a += partials[(size_t)r * K + k];
+    }
+    part[rt][lane] = a;
+    __syncthreads();
+    if (rt != 0 || k >= K) return;
+#pragma unroll
+    for (int r = 1; r < 8; ++r) a += part[r][lane];
     dweight[k] = s != nullptr ? a / s[k] : a;
 }
 
-int norm_threads(int K) {
-    const int t = (K / 8 + 31) / 32 * 32;
-    return t < 1024 ? t : 1024;
+int up32(int v) { return (v + 31) / 32 * 32; }
+
+// Threads per row for V chunks each.
+int norm_threads(int K, int V) { return up32((K + 8 * V - 1) / (8 * V)); }
+
+// Many rows: more than the SMs hold with one row each and 1024 threads per row.
+bool norm_many(int64_t M, int num_sms) { return M > 2 * num_sms; }
+
+template <bool Q8>
+void norm_launch(const NormArgs& a, int num_sms, cudaStream_t stream) {
+    const bool many = norm_many(a.M, num_sms);
+    const int V = many || a.K > 16384 ? 4 : a.K > 8192 ? 2 : 1;
+    const int T = norm_threads(a.K, V);
+    const int64_t cap = (int64_t)num_sms * (1024 / T > 1 ? 1024 / T : 1);
+    const int grid = (int)(a.M < cap || !many ? a.M : cap);
+    if (V == 1) rmsnorm_kernel<1, 1024, Q8><<<grid, T, 0, stream>>>(a);
+    else if (V == 2) rmsnorm_kernel<2, 1024, Q8><<<grid, T, 0, stream>>>(a);
+    else if (T <= 256) rmsnorm_kernel<4, 256, Q8><<<grid, T, 0, stream>>>(a);
+    else if (T <= 512) rmsnorm_kernel<4, 512, Q8><<<grid, T, 0, stream>>>(a);
+    else rmsnorm_kernel<4, 1024, Q8><<<grid, T, 0, stream>>>(a);
 }
 
-int norm_chunks(int K) { return (K / 8 + norm_threads(K) - 1) / norm_threads(K); }
+// The backward launch: chunks and threads per row, rows side by side per block, blocks.
+struct NormBwdPlan {
+    int V, T, groups, grid;
+};
 
-int norm_grid(int64_t M, int threads, int num_sms) {
-    const int64_t cap = (int64_t)num_sms * (2048 / threads < 8 ? 2048 / threads : 8);
-    return (int)(M < cap ? M : cap);
+NormBwdPlan norm_backward_plan(int64_t M, int K, int num_sms) {
+    NormBwdPlan b;
+    const bool many = norm_many(M, num_sms);
+    b.V = many || K > 16384 ? 4 : K > 8192 ? 2 : 1;
+    b.T = norm_threads(K, b.V);
+    b.groups = many && b.T <= 256 ? (512 / b.T < 4 ? 512 / b.T : 4) : 1;
+    const int64_t need = (M + b.groups - 1) / b.groups;
+    b.grid = (int)(need < num_sms ? need : num_sms);
+    return b;
 }
 
 }  // namespace
 
-int rmsnorm_backward_rows(int64_t M, int K, int num_sms) { return norm_grid(M, norm_threads(K), num_sms); }
+int rmsnorm_backward_rows(int64_t M, int K, int num_sms) { return norm_backward_plan(M, K, num_sms).grid; }
 
 cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
                            float eps, uint16_t* h, uint16_t* y, uint8_t* q, float* scales, int group, int64_t M, int K,
                            int num_sms, cudaStream_t stream) {
     const NormArgs a{x, residual, weight, s, eps, h, y, q, scales, group, M, K};
-    const int T = norm_threads(K), V = norm_chunks(K);
-    const int grid = norm_grid(M, T, num_sms);
-    if (q != nullptr) {
-        if (V == 1) rmsnorm_kernel<1, true><<<grid, T, 0, stream>>>(a);
-        else if (V == 2) rmsnorm_kernel<2, true><<<grid, T, 0, stream>>>(a);
-        else rmsnorm_kernel<4, true><<<grid, T, 0, stream>>>(a);
-    } else {
-        if (V == 1) rmsnorm_kernel<1, false><<<grid, T, 0, stream>>>(a);
-        else if (V == 2) rmsnorm_kernel<2, false><<<grid, T, 0, stream>>>(a);
-        else rmsnorm_kernel<4, false><<<grid, T, 0, stream>>>(a);
-    }
+    if (q != nullptr) norm_launch<true>(a, num_sms, stream);
+    else norm_launch<false>(a, num_sms, stream);
     return cudaGetLastError();
 }
 
@@ -298,14 +421,22 @@ cudaError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const
                                     const uint16_t* dh, float eps, uint16_t* dx, float* dweight, float* partials,
                                     int64_t M, int K, int num_sms, cudaStream_t stream) {
     const NormBwdArgs a{dy, h, weight, s, dh, eps, dx, dweight != nullptr ? partials : nullptr, M, K};
-    const int T = norm_threads(K), V = norm_chunks(K);
-    const int grid = rmsnorm_backward_rows(M, K, num_sms);
-    if (V == 1) rmsnorm_backward_kernel<1><<<grid, T, 0, stream>>>(a);
-    else if (V == 2) rmsnorm_backward_kernel<2><<<grid, T, 0, stream>>>(a);
-    else rmsnorm_backward_kernel<4><<<grid, T, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
+    const NormBwdPlan b = norm_backward_plan(M, K, num_sms);
+    const int threads = b.T * b.groups;
+    const size_t smem = (size_t)(b.groups - 1) * K * 4;
+    auto* fn = b.V == 1 ? rmsnorm_backward_kernel<1, 1024>
+               : b.V == 2 ? rmsnorm_backward_kernel<2, 1024>
+               : threads <= 512 ? rmsnorm_backward_kernel<4, 512>
+                                : rmsnorm_backward_kernel<4, 1024>;
+    cudaError_t e;
+    if (smem > 32 * 1024) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    fn<<<b.grid, threads, smem, stream>>>(a, b.T);
+    e = cudaGetLastError();
     if (e != cudaSuccess || dweight == nullptr) return e;
-    rmsnorm_dweight_kernel<<<(K + 255) / 256, 256, 0, stream>>>(partials, s, dweight, grid, K);
+    rmsnorm_dweight_kernel<<<(K + 31) / 32, 256, 0, stream>>>(partials, s, dweight, b.grid, K);
     return cudaGetLastError();
 }
 
