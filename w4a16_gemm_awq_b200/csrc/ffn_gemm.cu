@@ -13,9 +13,9 @@
 //     per product of a single-CTA tile of the same width.
 //   - The two accumulators (BN fp32 columns each, at TMEM columns 0 and 256) are used in turn, so the
 //     epilogue of one tile runs while the next one accumulates.
-//   - Warp roles (512 threads): 0 TMA of the activations, 1 MMA issue (leader CTA), 2 TMA of the
-//     packed weights, 3 TMEM allocation, 4-7 epilogue (one TMEM lane quarter each), 8-15 dequant:
-//     two groups of four warps, which take the stages of 64 contraction steps in turn.
+//   - Warp roles (640 threads): 0 TMA of the activations, 1 MMA issue (leader CTA), 2 TMA of the
+//     packed weights, 3 TMEM allocation, 4-7 epilogue (one TMEM lane quarter each), 8-19 dequant:
+//     three groups of four warps, which take the stages of 64 contraction steps in turn.
 //   - Dequant.  A ring entry holds the packed weights of 128 x 128 codes (8 KB, 64-byte rows, 64-byte
 //     swizzle).  A thread turns 8 words into 64 bf16 and stores them as 16-byte chunks of the A stage
 //     in the layout that the MMA reads, conflict-free.  Forward products contract over k, so a packed
@@ -43,7 +43,8 @@ namespace w4a16 {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kGroups = 3;               // dequant groups of four warps
+constexpr int kThreads = 32 * (8 + 4 * kGroups);
 constexpr int kS = 6;                    // stages of 64 contraction steps
 constexpr int kP = 4;                    // packed entries of 128 contraction steps
 constexpr int kABytes = 128 * 128;       // 128 channels x 64 steps, bf16
@@ -366,9 +367,12 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             // D fp32, A and B bf16, B K-major, A K-major or (backward) MN-major, M = 256, N = bn
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (MODE == kBackward ? 1u << 15 : 0u) |
                                    ((uint32_t)(p.bn >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
-            const uint32_t a0 = smem_u32(smem) + kAOff, b0 = smem_u32(smem) + kBOff;
+            const uint32_t base = smem_u32(smem);
+            const uint64_t a0 = MODE == kBackward ? smem_desc(base + kAOff, 8192, 1024) : smem_desc(base + kAOff, 16, 1024);
+            const uint64_t b0 = smem_desc(base + kBOff, 16, 1024);
+            constexpr uint32_t kAStep = (MODE == kBackward ? 2048 : 32) >> 4, kBStep = 32 >> 4;  // 16 steps, as descriptors count
             bool ok = true;
-            unsigned s = 0;
+            uint32_t slot = 0, phase = 0;
             for (unsigned t = 0; ok && walk_step(w, p, pair, pairs); ++t) {
                 const unsigned buf = t & 1;
                 const uint32_t d = tmem + buf * kTmemSecond;
@@ -376,25 +380,26 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                     ok = false;
                     break;
                 }
-                for (int c = 2 * w.e0; c < 2 * w.e1; ++c, ++s) {
-                    const unsigned slot = s % kS;
-                    if (!warp_wait(&full[slot], (s / kS) & 1)) {
+                const int stages = 2 * (w.e1 - w.e0);
+                for (int c = 0; c < stages; ++c) {
+                    if (!warp_wait(&full[slot], phase)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a = a0 + slot * kABytes, b = b0 + slot * kBBytes;
                     if (elect_one()) {
+                        const uint64_t a = a0 + slot * (kABytes >> 4), b = b0 + slot * (kBBytes >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const uint64_t ad = MODE == kBackward ? smem_desc(a + kk * 2048, 8192, 1024)
-                                                                  : smem_desc(a + kk * 32, 16, 1024);
-                            mma_pair(d, ad, smem_desc(b + kk * 32, 16, 1024), idesc, (c > 2 * w.e0 || kk > 0) ? 1u : 0u);
-                        }
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_pair(d, a + kk * kAStep, b + kk * kBStep, idesc, (c > 0 || kk > 0) ? 1u : 0u);
                         commit_pair(&empty[slot]);
-                        if (c == 2 * w.e1 - 1) commit_pair(&dfull[buf]);
+                        if (c == stages - 1) commit_pair(&dfull[buf]);
                     }
                     __syncwarp();
+                    if (++slot == kS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             if (!ok) {
@@ -405,50 +410,63 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         }
     } else if (warp >= 8) {
         // ---------------------------------------------------------------- dequant
-        const int group = (warp - 8) >> 2;          // takes stage 2 e + group of entry e
-        const int t = threadIdx.x & 127;
-        // forward: row t of A (for GATED 16 gate rows, 16 up rows, ...), half `group` of its 64 bytes;
-        // backward: step t % 64 of the stage, channels 64 (t / 64) .. + 63
-        const int prow = MODE == kLinear ? t
-                         : MODE == kGated ? ((t >> 4) & 1) * 64 + 16 * (t >> 5) + (t & 15)
-                                          : 64 * group + (t & 63);
-        const int half = MODE == kBackward ? t >> 6 : group;
-        const uint32_t src0 = prow * 64 + (((2 * half) ^ ((prow >> 1) & 3)) << 4);
-        const uint32_t src1 = prow * 64 + (((2 * half + 1) ^ ((prow >> 1) & 3)) << 4);
+        // The groups take the stages in turn.  A thread's packed words of its next stage are read before it
+        // dequantizes the current one, so that the wait for them and the loads stay out of the chain.
+        const int group = (warp - 8) >> 2;
+        const int t = threadIdx.x & 127;  // the first dequant warp is the first of four
+        int stages = 0;
+        while (walk_step(w, p, pair, pairs)) stages += 2 * (w.e1 - w.e0);
+        // forward: row t of A (for GATED 16 gate rows, 16 up rows, ...), the half of its 64 bytes that is the
+        // stage's; backward: step t % 64 of the stage's half of the packed rows, channels 64 (t / 64) .. + 63
         const int arow = MODE == kBackward ? (t & 63) : t;   // 128-byte row of the A stage
-        const uint32_t dst = (MODE == kBackward ? half * 8192 : 0) + arow * 128;
+        const uint32_t dst = (MODE == kBackward ? (t >> 6) * 8192 : 0) + arow * 128;
         const uint32_t sw = (arow & 7) << 4;
+        struct Packed {
+            uint4 a, b;
+            uint32_t scale, zword;
+        };
         bool ok = true;
-        unsigned i = 0;  // packed entries so far; stage 2 i + group
-        while (ok && walk_step(w, p, pair, pairs)) {
-            for (int e = w.e0; e < w.e1; ++e, ++i) {
-                const unsigned ps = i % kP;
-                if (!warp_wait(&pfull[ps], (i / kP) & 1)) {
-                    ok = false;
-                    break;
-                }
-                const uint8_t* src = smem + kPOff + ps * kEntryBytes;
-                const uint4 wa = *reinterpret_cast<const uint4*>(src + src0);
-                const uint4 wb = *reinterpret_cast<const uint4*>(src + src1);
-                const uint8_t* par = smem + kParOff + ps * kParBytes;
-                const uint16_t sbits = reinterpret_cast<const uint16_t*>(par)[prow];
-                const uint32_t zword = reinterpret_cast<const uint32_t*>(par + 256)[prow >> 3] >> (4 * (prow & 7));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&pempty[ps]);
-                const RowParams rp = row_params(sbits, zword & 15u);
-                const unsigned s = 2 * i + group, slot = s % kS;
-                if (s >= kS && !warp_wait(&empty[slot], (s / kS - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* a = smem + kAOff + slot * kABytes + dst;
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4*>(a + ((c << 4) ^ sw)) = dequant_word(c < 4 ? u4_get(wa, c) : u4_get(wb, c - 4), rp);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(cluster_map(&full[slot], 0));
+        auto fetch = [&](int s, Packed& q) {
+            const unsigned i = (unsigned)s >> 1, ps = i % kP;
+            const int h = s & 1;
+            const int prow = MODE == kLinear ? t
+                             : MODE == kGated ? ((t >> 4) & 1) * 64 + 16 * (t >> 5) + (t & 15)
+                                              : 64 * h + (t & 63);
+            const int half = MODE == kBackward ? t >> 6 : h;
+            if (!warp_wait(&pfull[ps], (i / kP) & 1)) return false;
+            const uint8_t* src = smem + kPOff + ps * kEntryBytes + prow * 64;
+            const int x = (prow >> 1) & 3;
+            q.a = *reinterpret_cast<const uint4*>(src + (((2 * half) ^ x) << 4));
+            q.b = *reinterpret_cast<const uint4*>(src + (((2 * half + 1) ^ x) << 4));
+            const uint8_t* par = smem + kParOff + ps * kParBytes;
+            q.scale = reinterpret_cast<const uint16_t*>(par)[prow];
+            q.zword = reinterpret_cast<const uint32_t*>(par + 256)[prow >> 3] >> (4 * (prow & 7));
+            return true;
+        };
+        Packed cur{}, next{};
+        if (group < stages) ok = fetch(group, cur);
+        for (int s = group; ok && s < stages; s += kGroups) {
+            const RowParams rp = row_params((uint16_t)cur.scale, cur.zword & 15u);  // the loads have arrived
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pempty[((unsigned)s >> 1) % kP]);
+            if (s + kGroups < stages && !fetch(s + kGroups, next)) {
+                ok = false;
+                break;
             }
+            const unsigned slot = (unsigned)s % kS;
+            if (s >= kS && !warp_wait(&empty[slot], ((unsigned)s / kS - 1) & 1)) {
+                ok = false;
+                break;
+            }
+            uint8_t* a = smem + kAOff + slot * kABytes + dst;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(a + ((c << 4) ^ sw)) =
+                    dequant_word(c < 4 ? u4_get(cur.a, c) : u4_get(cur.b, c - 4), rp);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(cluster_map(&full[slot], 0));
+            cur = next;
         }
         if (!ok && lane == 0) fail();
     } else if (warp >= 4) {
@@ -504,31 +522,33 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                                            : tc * 256 + rank * 128 + row;
             const int ld = MODE == kBackward ? p.K : p.N;
             const bool in = n < ld;
+            constexpr int C = MODE == kLinear ? 16 : 32;  // columns at a time; 16 leaves room for the residual
             float bias = 0.0f;
             if (MODE == kLinear && p.bias != nullptr && in) bias = bf16_bits_to_float(p.bias[n]);
 #pragma unroll 1
-            for (int c0 = 0; c0 < mlim; c0 += 32) {
-                float acc[32];
+            for (int c0 = 0; c0 < mlim; c0 += C) {
+                float acc[C];
                 if (w.partial) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[j] = __ldcg(part0 + (size_t)(c0 + j) * 128);
+                    for (int j = 0; j < C; ++j) acc[j] = __ldcg(part0 + (size_t)(c0 + j) * 128);
                     for (int q = 1; q < w.count; ++q)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[j] += __ldcg(part0 + q * part_step + (size_t)(c0 + j) * 128);
+                        for (int j = 0; j < C; ++j) acc[j] += __ldcg(part0 + q * part_step + (size_t)(c0 + j) * 128);
                 } else {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(d + (uint32_t)c0, r);
+                    uint32_t r[C];
+                    if constexpr (C == 32) tmem_ld_32x32b_x32(d + (uint32_t)c0, r);
+                    else tmem_ld_32x32b_x16(d + (uint32_t)c0, r);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[j] = __uint_as_float(r[j]);
+                    for (int j = 0; j < C; ++j) acc[j] = __uint_as_float(r[j]);
                 }
-                const int nj = mlim - c0;  // valid columns of this chunk (32 or more: all)
+                const int nj = mlim - c0;  // valid columns of this chunk (C or more: all)
                 const size_t o0 = (size_t)(m0 + c0) * ld + n;
                 if constexpr (MODE == kGated) {
                     if (p.pre != nullptr) {
                         uint16_t* o = (lane < 16 ? p.pre : p.pre2) + o0;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                        for (int j = 0; j < C; ++j)
                             if (j < nj) o[(size_t)j * ld] = float_to_bf16_bits(acc[j]);
                     }
                     // lanes below 16 finish tokens 0..15 of the chunk, the others 16..31
@@ -547,27 +567,27 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                         if (j0 + j < nj) p.y[o0 + (size_t)(j0 + j) * ld] = float_to_bf16_bits(g[j] * u[j]);
                 } else if (in) {
                     if constexpr (MODE == kLinear) {
-                        uint16_t res[32];
+                        uint16_t res[C];
                         if (p.residual != nullptr) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
+                            for (int j = 0; j < C; ++j)
                                 res[j] = j < nj ? p.residual[o0 + (size_t)j * ld] : (uint16_t)0;
                         }
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[j] += bias;
+                        for (int j = 0; j < C; ++j) acc[j] += bias;
                         if (p.pre != nullptr) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
+                            for (int j = 0; j < C; ++j)
                                 if (j < nj) p.pre[o0 + (size_t)j * ld] = float_to_bf16_bits(acc[j]);
                         }
                         act_values(p.act, acc);
                         if (p.residual != nullptr) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) acc[j] += bf16_bits_to_float(res[j]);
+                            for (int j = 0; j < C; ++j) acc[j] += bf16_bits_to_float(res[j]);
                         }
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < C; ++j)
                         if (j < nj) p.y[o0 + (size_t)j * ld] = float_to_bf16_bits(acc[j]);
                 }
             }
