@@ -218,9 +218,17 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// The whole warp waits; the result is the same in all its lanes.
+// The whole warp waits for a barrier phase, bounded in time.  Every branch goes by a vote, so the lanes
+// stay converged, as the .aligned instructions after a wait require.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const unsigned long long t0 = global_timer_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kWaitLimitNs)) return false;
+    }
 }
 
 // Barrier among the four epilogue warps.
@@ -308,6 +316,8 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 __syncwarp();
             }
         }
+        // every MMA has read its stage and said so in both CTAs before either may leave
+        for (unsigned i = s > kS ? s - kS : 0; ok && i < s; ++i) ok = warp_wait(&empty[i % kS], (i / kS) & 1);
         if (!ok && lane == 0) fail();
     } else if (warp == 2) {
         // ---------------------------------------------------------------- packed weights
@@ -373,7 +383,8 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             constexpr uint32_t kAStep = (MODE == kBackward ? 2048 : 32) >> 4, kBStep = 32 >> 4;  // 16 steps, as descriptors count
             bool ok = true;
             uint32_t slot = 0, phase = 0;
-            for (unsigned t = 0; ok && walk_step(w, p, pair, pairs); ++t) {
+            unsigned t = 0;
+            for (; ok && walk_step(w, p, pair, pairs); ++t) {
                 const unsigned buf = t & 1;
                 const uint32_t d = tmem + buf * kTmemSecond;
                 if (t >= 2 && !warp_wait(&dempty[buf], (t / 2 - 1) & 1)) {
@@ -402,6 +413,8 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                     }
                 }
             }
+            // the other CTA's last arrivals are here before this one may leave
+            for (unsigned i = t > 2 ? t - 2 : 0; ok && i < t; ++i) ok = warp_wait(&dempty[i & 1], (i / 2) & 1);
             if (!ok) {
                 if (lane == 0) fail();
                 if (elect_one()) commit_pair(drain);  // MMAs in flight finish first
