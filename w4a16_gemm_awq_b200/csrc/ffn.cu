@@ -42,6 +42,7 @@ template <int ACT>
 __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_kernel(const uint16_t* dy, const uint16_t* pre,
                                                                        uint16_t* dp, float* sums, float* dbias,
                                                                        unsigned* counters, long long M, int N, int rows) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
     __shared__ float part[kDpRowThreads][kDpCols];
     __shared__ int last;
     const int lane = threadIdx.x & 31, rt = threadIdx.x >> 5;
@@ -88,6 +89,7 @@ __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_kernel(const uin
     if (!last || nc >= N) return;
     __threadfence();
     s = 0.0f;
+#pragma unroll 8
     for (int r = 0; r < (int)gridDim.y; ++r) s += __ldcg(sums + (size_t)r * N + nc);
     dbias[nc] = s;
 }
@@ -96,6 +98,7 @@ __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_kernel(const uin
 template <int ACT>
 __global__ void __launch_bounds__(256) gated_dp_kernel(const uint4* dh, const uint4* g, const uint4* u, uint4* dg,
                                                        uint4* du, long long n) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
         float d[8], a[8], b[8], x[8], y[8];
         unpack8(__ldcs(dh + i), d);
@@ -113,9 +116,9 @@ __global__ void __launch_bounds__(256) gated_dp_kernel(const uint4* dh, const ui
 
 }  // namespace
 
-// Runs of rows: enough blocks for a few per SM, at least 8 rows each, and few enough that adding the
-// runs up (N threads, one load per run) stays short.
-int linear_dp_blocks(int64_t M) { return (int)((M + 15) / 16 < 64 ? (M + 15) / 16 : 64); }
+// Runs of rows: at least 16 rows each, and few enough that adding the runs up (N threads, one load per
+// run) stays short.  (64 runs at 1023 x 5120 took 20 us, most of it in the last blocks' sums.)
+int linear_dp_blocks(int64_t M) { return (int)((M + 15) / 16 < 32 ? (M + 15) / 16 : 32); }
 
 cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* dbias, float* sums,
                              unsigned* counters, int64_t M, int N, int act, cudaStream_t stream) {

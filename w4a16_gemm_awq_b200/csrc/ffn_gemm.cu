@@ -46,7 +46,7 @@ namespace {
 constexpr int kGroups = 3;               // dequant groups of four warps
 constexpr int kThreads = 32 * (8 + 4 * kGroups);
 constexpr int kS = 6;                    // stages of 64 contraction steps
-constexpr int kP = 4;                    // packed entries of 128 contraction steps
+constexpr int kP = 3;                    // packed entries of 128 contraction steps
 constexpr int kABytes = 128 * 128;       // 128 channels x 64 steps, bf16
 constexpr int kBBytes = 128 * 128;       // up to 128 tokens (this CTA's half) x 64 steps, bf16
 constexpr int kEntryBytes = 128 * 64;    // 128 packed rows of 16 words
@@ -55,7 +55,11 @@ constexpr int kAOff = 0;
 constexpr int kBOff = kAOff + kS * kABytes;
 constexpr int kPOff = kBOff + kS * kBBytes;
 constexpr int kParOff = kPOff + kP * kEntryBytes;
-constexpr int kBarOff = kParOff + kP * kParBytes;
+constexpr int kOutCols = 16;             // columns (tokens) an epilogue warp finishes at a time
+constexpr int kOutStride = 36;           // floats per token in its transposing buffer: 32 channels, padded
+constexpr int kOutOff = kParOff + kP * kParBytes;
+constexpr int kOutBytes = kOutCols * kOutStride * 4;
+constexpr int kBarOff = kOutOff + 4 * kOutBytes;
 constexpr int kSmemBytes = kBarOff + 256;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 constexpr uint32_t kTmemCols = 512;
@@ -211,6 +215,13 @@ __device__ __forceinline__ uint4 dequant_word(uint32_t word, const RowParams& r)
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -277,6 +288,8 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         mbar_init(drain, 1);
         fence_mbarrier_init();
     }
+    if (warp == 0) prefetch_tensormap(&map_x);
+    if (warp == 2) prefetch_tensormap(&map_w);
     if (warp == 3) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(kTmemCols) : "memory");
@@ -284,19 +297,70 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();  // the other CTA's barriers are initialised too
-    tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    // The next kernel on the stream may be scheduled as this one's CTAs leave; what it must not do before
+    // this one is complete comes after its own griddepcontrol.wait.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     auto fail = [&]() { record_error(p.err, kErrTimeout); };
     Walk w = walk_start(p, pair);
+
+    // One packed entry: 64 packed rows from n with their scales and zero points to each half of the slot.
+    auto load_entry = [&](unsigned slot, int tile, int e) {
+        const int tc = tile % p.tiles_c;
+        uint8_t* dst = smem + kPOff + slot * kEntryBytes;
+        uint8_t* par = smem + kParOff + slot * kParBytes;
+        auto load = [&](int hh, const CUtensorMap* map, const PackedWeights& q, int word, int n, int g) {
+            tma_load_2d(dst + hh * (kEntryBytes / 2), map, &pfull[slot], word, n);
+            bulk_load(par + 128 * hh, q.scales + (size_t)g * p.N + n, 128, &pfull[slot]);
+            bulk_load(par + 256 + 32 * hh, q.zeros + (size_t)g * (p.N >> 3) + (n >> 3), 32, &pfull[slot]);
+        };
+        if (MODE == kLinear) {
+            // the last pair's second half may be past N: its rows go nowhere
+            const int n = tc * 256 + rank * 128;
+            const bool in = n < p.N;
+            mbar_arrive_expect_tx(&pfull[slot], in ? kEntryBytes + 320 : 16);
+            if (in) {
+                load(0, &map_w, p.w, e * 16, n, e / p.gr);
+                load(1, &map_w, p.w, e * 16, n + 64, e / p.gr);
+            } else {
+                bulk_load(par, p.w.scales, 16, &pfull[slot]);
+            }
+        } else if (MODE == kGated) {
+            const int n = tc * 128 + rank * 64;
+            mbar_arrive_expect_tx(&pfull[slot], kEntryBytes + 320);
+            load(0, &map_w, p.w, e * 16, n, e / p.gr);
+            load(1, &map_w2, p.w2, e * 16, n, e / p.gr);
+        } else {
+            const int kt = tc * 2 + rank;
+            mbar_arrive_expect_tx(&pfull[slot], kEntryBytes + 320);
+            if (e < p.entries1) {
+                load(0, &map_w, p.w, kt * 16, e * 128, kt / p.gr);
+                load(1, &map_w, p.w, kt * 16, e * 128 + 64, kt / p.gr);
+            } else {
+                load(0, &map_w2, p.w2, kt * 16, (e - p.entries1) * 128, kt / p.gr);
+                load(1, &map_w2, p.w2, kt * 16, (e - p.entries1) * 128 + 64, kt / p.gr);
+            }
+        }
+    };
+    // The first packed entries are what a call waits for first, and they need only this CTA's barriers.
+    // (No kernel before this one on the stream writes the weights.)
+    if (warp == 2) {
+        Walk first = w;
+        if (walk_step(first, p, pair, pairs) && elect_one()) {
+            for (int i = 0; i < kP && first.e0 + i < first.e1; ++i) load_entry(i, first.tile, first.e0 + i);
+        }
+        __syncwarp();
+    }
+    cluster_sync_all();  // the other CTA's barriers are initialised too
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     // The TMA and MMA warps run their loops as whole warps and issue from one elected lane: the operands
     // of those instructions sit in uniform registers, and a loop that one lane runs alone moves each of
     // them there every time (385 to 480 cycles to issue a stage's four MMAs).
     if (warp == 0) {
         // ---------------------------------------------------------------- activations
-        prefetch_tensormap(&map_x);
+        griddep_wait();  // the activations belong to the stream order
         bool ok = true;
         unsigned s = 0;
         while (ok && walk_step(w, p, pair, pairs)) {
@@ -309,9 +373,11 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 }
                 if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)p.bn * 128u);
-                    const bool second = MODE == kBackward && c >= 2 * p.entries1;
-                    tma_load_2d_pair(smem + kBOff + slot * kBBytes, second ? &map_x2 : &map_x,
-                                     cluster_map(&full[slot], 0), (second ? c - 2 * p.entries1 : c) * 64, m0);
+                    uint8_t* dst = smem + kBOff + slot * kBBytes;
+                    if (MODE == kBackward && c >= 2 * p.entries1)
+                        tma_load_2d_pair(dst, &map_x2, cluster_map(&full[slot], 0), (c - 2 * p.entries1) * 64, m0);
+                    else
+                        tma_load_2d_pair(dst, &map_x, cluster_map(&full[slot], 0), c * 64, m0);
                 }
                 __syncwarp();
             }
@@ -321,52 +387,17 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         if (!ok && lane == 0) fail();
     } else if (warp == 2) {
         // ---------------------------------------------------------------- packed weights
-        prefetch_tensormap(&map_w);
         bool ok = true;
         unsigned i = 0;
-        while (ok && walk_step(w, p, pair, pairs)) {
-            const int tc = w.tile % p.tiles_c;
+        for (bool begun = false; ok && walk_step(w, p, pair, pairs); begun = true) {
             for (int e = w.e0; e < w.e1; ++e, ++i) {
+                if (!begun && i < kP) continue;  // loaded above
                 const unsigned slot = i % kP;
                 if (i >= kP && !warp_wait(&pempty[slot], (i / kP - 1) & 1)) {
                     ok = false;
                     break;
                 }
-                uint8_t* dst = smem + kPOff + slot * kEntryBytes;
-                uint8_t* par = smem + kParOff + slot * kParBytes;
-                // 64 packed rows from n with their scales and zero points, to half hh of the entry
-                auto load = [&](int hh, const CUtensorMap* map, const PackedWeights& q, int word, int n, int g) {
-                    tma_load_2d(dst + hh * (kEntryBytes / 2), map, &pfull[slot], word, n);
-                    bulk_load(par + 128 * hh, q.scales + (size_t)g * p.N + n, 128, &pfull[slot]);
-                    bulk_load(par + 256 + 32 * hh, q.zeros + (size_t)g * (p.N >> 3) + (n >> 3), 32, &pfull[slot]);
-                };
-                if (elect_one()) {
-                    if (MODE == kLinear) {
-                        // the last pair's second half may be past N: its rows go nowhere
-                        const int n = tc * 256 + rank * 128;
-                        const bool in = n < p.N;
-                        mbar_arrive_expect_tx(&pfull[slot], in ? kEntryBytes + 320 : 16);
-                        if (in) {
-                            load(0, &map_w, p.w, e * 16, n, e / p.gr);
-                            load(1, &map_w, p.w, e * 16, n + 64, e / p.gr);
-                        } else {
-                            bulk_load(par, p.w.scales, 16, &pfull[slot]);
-                        }
-                    } else if (MODE == kGated) {
-                        const int n = tc * 128 + rank * 64;
-                        mbar_arrive_expect_tx(&pfull[slot], kEntryBytes + 320);
-                        load(0, &map_w, p.w, e * 16, n, e / p.gr);
-                        load(1, &map_w2, p.w2, e * 16, n, e / p.gr);
-                    } else {
-                        const bool second = e >= p.entries1;
-                        const CUtensorMap* map = second ? &map_w2 : &map_w;
-                        const PackedWeights& q = second ? p.w2 : p.w;
-                        const int n = (second ? e - p.entries1 : e) * 128, kt = tc * 2 + rank;
-                        mbar_arrive_expect_tx(&pfull[slot], kEntryBytes + 320);
-                        load(0, map, q, kt * 16, n, kt / p.gr);
-                        load(1, map, q, kt * 16, n + 64, kt / p.gr);
-                    }
-                }
+                if (elect_one()) load_entry(slot, w.tile, e);
                 __syncwarp();
             }
         }
@@ -454,14 +485,14 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             const uint8_t* par = smem + kParOff + ps * kParBytes;
             q.scale = reinterpret_cast<const uint16_t*>(par)[prow];
             q.zword = reinterpret_cast<const uint32_t*>(par + 256)[prow >> 3] >> (4 * (prow & 7));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pempty[ps]);
             return true;
         };
         Packed cur{}, next{};
         if (group < stages) ok = fetch(group, cur);
         for (int s = group; ok && s < stages; s += kGroups) {
-            const RowParams rp = row_params((uint16_t)cur.scale, cur.zword & 15u);  // the loads have arrived
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pempty[((unsigned)s >> 1) % kP]);
+            const RowParams rp = row_params((uint16_t)cur.scale, cur.zword & 15u);
             if (s + kGroups < stages && !fetch(s + kGroups, next)) {
                 ok = false;
                 break;
@@ -487,6 +518,8 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         const int quarter = warp & 3;
         const int row = 32 * quarter + lane;  // TMEM lane
         const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
+        float* const out = reinterpret_cast<float*>(smem + kOutOff + quarter * kOutBytes);
+        griddep_wait();  // the residual, the outputs and the workspace belong to the stream order
         bool ok = true;
         for (unsigned t = 0; walk_step(w, p, pair, pairs); ++t) {
             const unsigned buf = t & 1;
@@ -530,79 +563,99 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 if (!last) continue;
                 __threadfence();
             }
-            const int n = MODE == kLinear ? tc * 256 + rank * 128 + row
-                          : MODE == kGated ? tc * 128 + rank * 64 + 16 * quarter + (lane & 15)
-                                           : tc * 256 + rank * 128 + row;
+            // A lane holds one channel of 16 tokens; through the warp's buffer it gets 4 neighbouring channels
+            // of one token at a time, so that the outputs and the residual move 8 bytes at a time: LINEAR and
+            // BACKWARD 8 lanes per token (32 channels), GATED 4 (16 channels, gate and up).
+            constexpr int kLanes = MODE == kGated ? 4 : 8, kTok = 32 / kLanes, kIts = kOutCols / kTok;
+            const int ch = 4 * (lane % kLanes), tk = lane / kLanes;
+            const int n = MODE == kGated ? tc * 128 + rank * 64 + 16 * quarter + ch : tc * 256 + rank * 128 + 32 * quarter + ch;
             const int ld = MODE == kBackward ? p.K : p.N;
-            const bool in = n < ld;
-            constexpr int C = MODE == kLinear ? 16 : 32;  // columns at a time; 16 leaves room for the residual
+            const bool in = n < ld;  // the last pair's second half may be past N (whole warps)
             float bias = 0.0f;
-            if (MODE == kLinear && p.bias != nullptr && in) bias = bf16_bits_to_float(p.bias[n]);
+            if (MODE == kLinear && p.bias != nullptr && in) bias = bf16_bits_to_float(p.bias[n - ch + lane]);
 #pragma unroll 1
-            for (int c0 = 0; c0 < mlim; c0 += C) {
-                float acc[C];
+            for (int c0 = 0; c0 < mlim; c0 += kOutCols) {
+                const size_t o0 = (size_t)(m0 + c0 + tk) * ld + n;
+                const size_t step = (size_t)kTok * ld;
+                uint2 res[kIts];
+                if (MODE == kLinear && p.residual != nullptr && in) {
+#pragma unroll
+                    for (int i = 0; i < kIts; ++i)
+                        if (c0 + tk + i * kTok < mlim) res[i] = *reinterpret_cast<const uint2*>(p.residual + o0 + i * step);
+                }
+                float acc[kOutCols];
                 if (w.partial) {
+                    // the contributors' partial tiles in order, two at a time in flight
+                    const float* src = part0 + (size_t)c0 * 128;
 #pragma unroll
-                    for (int j = 0; j < C; ++j) acc[j] = __ldcg(part0 + (size_t)(c0 + j) * 128);
-                    for (int q = 1; q < w.count; ++q)
+                    for (int j = 0; j < kOutCols; ++j) acc[j] = __ldcg(src + j * 128);
+#pragma unroll 1
+                    for (int q = 1; q < w.count; ++q) {
+                        src += part_step;
+                        float v[kOutCols];
 #pragma unroll
-                        for (int j = 0; j < C; ++j) acc[j] += __ldcg(part0 + q * part_step + (size_t)(c0 + j) * 128);
+                        for (int j = 0; j < kOutCols; ++j) v[j] = __ldcg(src + j * 128);
+#pragma unroll
+                        for (int j = 0; j < kOutCols; ++j) acc[j] += v[j];
+                    }
                 } else {
-                    uint32_t r[C];
-                    if constexpr (C == 32) tmem_ld_32x32b_x32(d + (uint32_t)c0, r);
-                    else tmem_ld_32x32b_x16(d + (uint32_t)c0, r);
+                    uint32_t r[kOutCols];
+                    tmem_ld_32x32b_x16(d + (uint32_t)c0, r);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < C; ++j) acc[j] = __uint_as_float(r[j]);
+                    for (int j = 0; j < kOutCols; ++j) acc[j] = __uint_as_float(r[j]);
                 }
-                const int nj = mlim - c0;  // valid columns of this chunk (C or more: all)
-                const size_t o0 = (size_t)(m0 + c0) * ld + n;
+                __syncwarp();  // the previous columns have left the buffer
+#pragma unroll
+                for (int j = 0; j < kOutCols; ++j) out[j * kOutStride + lane] = acc[j] + bias;
+                __syncwarp();
+                float v[4 * kIts];
+#pragma unroll
+                for (int i = 0; i < kIts; ++i) {
+                    const float4 a = *reinterpret_cast<const float4*>(out + (tk + i * kTok) * kOutStride + ch);
+                    v[4 * i] = a.x;
+                    v[4 * i + 1] = a.y;
+                    v[4 * i + 2] = a.z;
+                    v[4 * i + 3] = a.w;
+                }
+                auto put = [&](uint16_t* dst, const float (&f)[4 * kIts]) {
+#pragma unroll
+                    for (int i = 0; i < kIts; ++i)
+                        if (in && c0 + tk + i * kTok < mlim)
+                            *reinterpret_cast<uint2*>(dst + o0 + i * step) =
+                                make_uint2(bf16x2_of(f[4 * i], f[4 * i + 1]), bf16x2_of(f[4 * i + 2], f[4 * i + 3]));
+                };
                 if constexpr (MODE == kGated) {
+                    float u[4 * kIts];
+#pragma unroll
+                    for (int i = 0; i < kIts; ++i) {
+                        const float4 a = *reinterpret_cast<const float4*>(out + (tk + i * kTok) * kOutStride + 16 + ch);
+                        u[4 * i] = a.x;
+                        u[4 * i + 1] = a.y;
+                        u[4 * i + 2] = a.z;
+                        u[4 * i + 3] = a.w;
+                    }
                     if (p.pre != nullptr) {
-                        uint16_t* o = (lane < 16 ? p.pre : p.pre2) + o0;
-#pragma unroll
-                        for (int j = 0; j < C; ++j)
-                            if (j < nj) o[(size_t)j * ld] = float_to_bf16_bits(acc[j]);
+                        put(p.pre, v);
+                        put(p.pre2, u);
                     }
-                    // lanes below 16 finish tokens 0..15 of the chunk, the others 16..31
-                    const bool low = lane < 16;
-                    const int j0 = low ? 0 : 16;
-                    float g[16], u[16];
+                    act_values(p.act, v);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float got = __shfl_xor_sync(0xffffffffu, low ? acc[j + 16] : acc[j], 16);
-                        g[j] = low ? acc[j] : got;
-                        u[j] = low ? got : acc[j + 16];
-                    }
-                    act_values(p.act, g);
+                    for (int i = 0; i < 4 * kIts; ++i) v[i] *= u[i];
+                } else if constexpr (MODE == kLinear) {
+                    if (p.pre != nullptr) put(p.pre, v);
+                    act_values(p.act, v);
+                    if (p.residual != nullptr) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j0 + j < nj) p.y[o0 + (size_t)(j0 + j) * ld] = float_to_bf16_bits(g[j] * u[j]);
-                } else if (in) {
-                    if constexpr (MODE == kLinear) {
-                        uint16_t res[C];
-                        if (p.residual != nullptr) {
-#pragma unroll
-                            for (int j = 0; j < C; ++j)
-                                res[j] = j < nj ? p.residual[o0 + (size_t)j * ld] : (uint16_t)0;
-                        }
-#pragma unroll
-                        for (int j = 0; j < C; ++j) acc[j] += bias;
-                        if (p.pre != nullptr) {
-#pragma unroll
-                            for (int j = 0; j < C; ++j)
-                                if (j < nj) p.pre[o0 + (size_t)j * ld] = float_to_bf16_bits(acc[j]);
-                        }
-                        act_values(p.act, acc);
-                        if (p.residual != nullptr) {
-#pragma unroll
-                            for (int j = 0; j < C; ++j) acc[j] += bf16_bits_to_float(res[j]);
+                        for (int i = 0; i < kIts; ++i) {
+                            v[4 * i] += __uint_as_float(res[i].x << 16);
+                            v[4 * i + 1] += __uint_as_float(res[i].x & 0xFFFF0000u);
+                            v[4 * i + 2] += __uint_as_float(res[i].y << 16);
+                            v[4 * i + 3] += __uint_as_float(res[i].y & 0xFFFF0000u);
                         }
                     }
-#pragma unroll
-                    for (int j = 0; j < C; ++j)
-                        if (j < nj) p.y[o0 + (size_t)j * ld] = float_to_bf16_bits(acc[j]);
                 }
+                put(p.y, v);
             }
             if (!w.partial) {
                 tc_fence_before();
@@ -632,19 +685,29 @@ FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms) {
     g.tiles_c = (rows + 255) / 256;
     g.tiles = (int64_t)g.tiles_c * ((M + g.bn - 1) / g.bn);
     const int rest = (int)(g.tiles % g.pairs);
-    // Cycles: a stage takes the longer of its MMAs and its dequant; joining a contributor's partial
-    // tile (512 bn bytes per CTA, written and read once) about 10 bn + 1500, and 3000 at the end.
-    const double stage = std::max(2.0 * g.bn, 240.0);
-    double best = 2.0 * entries * stage;
+    // Cycles of the last round and the cut tiles: a stage takes the longer of its MMAs and its dequant;
+    // joining a contributor's partial tile (512 bn bytes per CTA, written and read once) about 4 bn + 800,
+    // and 3000 for the count.  The rest alone may be cut (n runs per tile, at most one per pair), or the
+    // rest and one full round (one run per pair), which levels the pairs when the rest is small.
+    const double stage = std::max(1.45 * g.bn + 130.0, 440.0), tile = 2.0 * entries * stage;
+    double best = rest > 0 ? tile : 0.0;
     for (int n = 2; rest > 0 && n <= 16; ++n) {
         const int runs = std::min(g.pairs, rest * n);
         const int units = rest * entries;
         if (units / runs < 2) break;
-        const double cost = 2.0 * stage * units / runs + (10.0 * g.bn + 1500.0) * n + 3000.0;
+        const double cost = 2.0 * stage * units / runs + (4.0 * g.bn + 800.0) * n + 3000.0;
         if (cost < best) {
             best = cost;
             g.cut = rest;
             g.runs = runs;
+        }
+    }
+    if (rest > 0 && g.tiles > g.pairs) {
+        const double share = (double)(rest + g.pairs) / g.pairs;  // tiles per pair
+        const double cost = (share - 1.0) * tile + (4.0 * g.bn + 800.0) * 3 + 3000.0;
+        if (cost < best) {
+            g.cut = rest + g.pairs;
+            g.runs = g.pairs;
         }
     }
     g.partial_bytes = (size_t)(g.cut + g.runs) * 2 * 128 * g.bn * 4;
@@ -681,8 +744,17 @@ cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnA
     if (e != cudaSuccess) return e;
     const int64_t busy = plan.tiles > plan.cut ? std::max<int64_t>(plan.tiles - plan.cut, plan.runs) : plan.runs;
     const int pairs = (int)std::min<int64_t>(plan.pairs, busy);
-    fn<<<2 * pairs, kThreads, kSmemBytes, stream>>>(maps.x, maps.x2, maps.w, maps.w2, g);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, maps.x, maps.x2, maps.w, maps.w2, g);
 }
 
 }  // namespace w4a16
