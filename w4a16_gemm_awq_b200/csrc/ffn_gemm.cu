@@ -13,9 +13,10 @@
 //     per product of a single-CTA tile of the same width.
 //   - The two accumulators (BN fp32 columns each, at TMEM columns 0 and 256) are used in turn, so the
 //     epilogue of one tile runs while the next one accumulates.
-//   - Warp roles (640 threads): 0 TMA of the activations, 1 MMA issue (leader CTA), 2 TMA of the
-//     packed weights, 3 TMEM allocation, 4-7 epilogue (one TMEM lane quarter each), 8-19 dequant:
-//     three groups of four warps, which take the stages of 64 contraction steps in turn.
+//   - Warp roles (768 threads): 0 TMA of the activations, 1 MMA issue (leader CTA), 2 TMA of the
+//     packed weights, 3 TMEM allocation, 4-11 epilogue (a TMEM lane quarter and half of the columns
+//     each), 12-23 dequant: three groups of four warps, which take the stages of 64 contraction steps
+//     in turn.
 //   - Dequant.  A ring entry holds the packed weights of 128 x 128 codes (8 KB, 64-byte rows, 64-byte
 //     swizzle).  A thread turns 8 words into 64 bf16 and stores them as 16-byte chunks of the A stage
 //     in the layout that the MMA reads, conflict-free.  Forward products contract over k, so a packed
@@ -44,7 +45,8 @@ namespace w4a16 {
 namespace {
 
 constexpr int kGroups = 3;               // dequant groups of four warps
-constexpr int kThreads = 32 * (8 + 4 * kGroups);
+constexpr int kEpilogue0 = 4, kDequant0 = 12;
+constexpr int kThreads = 32 * (kDequant0 + 4 * kGroups);
 constexpr int kS = 6;                    // stages of 64 contraction steps
 constexpr int kP = 3;                    // packed entries of 128 contraction steps
 constexpr int kABytes = 128 * 128;       // 128 channels x 64 steps, bf16
@@ -55,11 +57,11 @@ constexpr int kAOff = 0;
 constexpr int kBOff = kAOff + kS * kABytes;
 constexpr int kPOff = kBOff + kS * kBBytes;
 constexpr int kParOff = kPOff + kP * kEntryBytes;
-constexpr int kOutCols = 16;             // columns (tokens) an epilogue warp finishes at a time
+constexpr int kOutCols = 8;              // columns (tokens) an epilogue warp finishes at a time
 constexpr int kOutStride = 36;           // floats per token in its transposing buffer: 32 channels, padded
 constexpr int kOutOff = kParOff + kP * kParBytes;
 constexpr int kOutBytes = kOutCols * kOutStride * 4;
-constexpr int kBarOff = kOutOff + 4 * kOutBytes;
+constexpr int kBarOff = kOutOff + 8 * kOutBytes;
 constexpr int kSmemBytes = kBarOff + 256;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 constexpr uint32_t kTmemCols = 512;
@@ -242,8 +244,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
     }
 }
 
-// Barrier among the four epilogue warps.
-__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barrier among the epilogue warps.
+__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
@@ -283,7 +285,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&dfull[i], 1);
-            mbar_init(&dempty[i], 8);  // four epilogue warps of each CTA
+            mbar_init(&dempty[i], 16);  // eight epilogue warps of each CTA
         }
         mbar_init(drain, 1);
         fence_mbarrier_init();
@@ -452,11 +454,11 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 (void)warp_wait(drain, 0);
             }
         }
-    } else if (warp >= 8) {
+    } else if (warp >= kDequant0) {
         // ---------------------------------------------------------------- dequant
         // The groups take the stages in turn.  A thread's packed words of its next stage are read before it
         // dequantizes the current one, so that the wait for them and the loads stay out of the chain.
-        const int group = (warp - 8) >> 2;
+        const int group = (warp - kDequant0) >> 2;
         const int t = threadIdx.x & 127;  // the first dequant warp is the first of four
         int stages = 0;
         while (walk_step(w, p, pair, pairs)) stages += 2 * (w.e1 - w.e0);
@@ -513,12 +515,13 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             cur = next;
         }
         if (!ok && lane == 0) fail();
-    } else if (warp >= 4) {
+    } else if (warp >= kEpilogue0) {
         // ---------------------------------------------------------------- epilogue
         const int quarter = warp & 3;
         const int row = 32 * quarter + lane;  // TMEM lane
         const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
-        float* const out = reinterpret_cast<float*>(smem + kOutOff + quarter * kOutBytes);
+        const int side = (warp - kEpilogue0) >> 2;  // which half of the columns
+        float* const out = reinterpret_cast<float*>(smem + kOutOff + (warp - kEpilogue0) * kOutBytes);
         griddep_wait();  // the residual, the outputs and the workspace belong to the stream order
         bool ok = true;
         for (unsigned t = 0; walk_step(w, p, pair, pairs); ++t) {
@@ -531,39 +534,50 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             const uint32_t d = tmem + t_lane + buf * kTmemSecond;
             const int tc = w.tile % p.tiles_c;
             const int m0 = (w.tile / p.tiles_c) * p.bn;
-            const int mlim = min(p.bn, p.M - m0);  // tokens of this tile
+            const int mtile = min(p.bn, p.M - m0);  // tokens of this tile
+            const int mid = ((mtile + 31) >> 5) << 4;  // columns of the first side, a multiple of 16
+            const int cb = side ? min(mid, mtile) : 0, mlim = side ? mtile : min(mid, mtile);  // this warp's
             // partial tiles, token-major: [run + tile][rank][bn][128]
             float* part0 = p.partials + ((size_t)(w.first + w.tile) * 2 + rank) * p.bn * 128 + row;
             const size_t part_step = (size_t)2 * p.bn * 128;
             if (w.partial) {
-                float* mine = part0 + w.index * part_step;
+                // A contributor that finds all the others counted joins them with its own accumulator; any
+                // other publishes its partial tile first and then counts itself, and joins if that made it
+                // the last.  The sum goes by the order of the runs either way, so its bits do not depend on
+                // who joins.
+                unsigned* counter = p.counters + 2 * w.tile + rank;
+                const unsigned others = (unsigned)(w.count - 1);
+                if (warp == kEpilogue0 && lane == 0) *last_flag = ld_acquire_gpu(counter) == others;
+                epilogue_barrier();
+                bool last = *reinterpret_cast<volatile int*>(last_flag) != 0;
+                epilogue_barrier();
+                if (!last) {
+                    float* mine = part0 + w.index * part_step;
 #pragma unroll 1
-                for (int c0 = 0; c0 < mlim; c0 += 32) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(d + (uint32_t)c0, r);
-                    tmem_ld_wait();
+                    for (int c0 = cb; c0 < mlim; c0 += 16) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(d + (uint32_t)c0, r);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) __stcg(mine + (size_t)(c0 + j) * 128, __uint_as_float(r[j]));
+                        for (int j = 0; j < 16; ++j) __stcg(mine + (size_t)(c0 + j) * 128, __uint_as_float(r[j]));
+                    }
+                    __threadfence();
+                    epilogue_barrier();
+                    if (warp == kEpilogue0 && lane == 0) *last_flag = atomic_add_acq_rel_gpu(counter, 1u) == others;
+                    epilogue_barrier();
+                    last = *reinterpret_cast<volatile int*>(last_flag) != 0;
+                    epilogue_barrier();
+                    if (!last) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_pair(cluster_map(&dempty[buf], 0));
+                        continue;
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(cluster_map(&dempty[buf], 0));
-                // the partial tile is published by the counter; the last to count itself joins all
-                __threadfence();
-                epilogue_barrier();
-                if (warp == 4 && lane == 0) {
-                    unsigned* counter = p.counters + 2 * w.tile + rank;
-                    const bool last = atomic_add_acq_rel_gpu(counter, 1u) == (unsigned)(w.count - 1);
-                    if (last) atomicExch(counter, 0u);
-                    *last_flag = last;
-                }
-                epilogue_barrier();
-                const bool last = *reinterpret_cast<volatile int*>(last_flag) != 0;
-                epilogue_barrier();
-                if (!last) continue;
+                if (warp == kEpilogue0 && lane == 0) atomicExch(counter, 0u);  // all have counted themselves
                 __threadfence();
             }
-            // A lane holds one channel of 16 tokens; through the warp's buffer it gets 4 neighbouring channels
+            // A lane holds one channel of 8 tokens; through the warp's buffer it gets 4 neighbouring channels
             // of one token at a time, so that the outputs and the residual move 8 bytes at a time: LINEAR and
             // BACKWARD 8 lanes per token (32 channels), GATED 4 (16 channels, gate and up).
             constexpr int kLanes = MODE == kGated ? 4 : 8, kTok = 32 / kLanes, kIts = kOutCols / kTok;
@@ -573,8 +587,23 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             const bool in = n < ld;  // the last pair's second half may be past N (whole warps)
             float bias = 0.0f;
             if (MODE == kLinear && p.bias != nullptr && in) bias = bf16_bits_to_float(p.bias[n - ch + lane]);
+            // the partial tiles of the first two other contributors, fetched one chunk ahead (those after them
+            // are rare)
+            float x0[kOutCols], x1[kOutCols];
+            const float* s0 = part0 + (w.index == 0 ? part_step : 0);
+            const float* s1 = part0 + (w.index <= 1 ? 2 * part_step : part_step);
+            auto fetch = [&](int c0) {
+                if (!w.partial || c0 >= mlim) return;
+#pragma unroll
+                for (int j = 0; j < kOutCols; ++j) x0[j] = __ldcg(s0 + (size_t)(c0 + j) * 128);
+                if (w.count > 2) {
+#pragma unroll
+                    for (int j = 0; j < kOutCols; ++j) x1[j] = __ldcg(s1 + (size_t)(c0 + j) * 128);
+                }
+            };
+            fetch(cb);
 #pragma unroll 1
-            for (int c0 = 0; c0 < mlim; c0 += kOutCols) {
+            for (int c0 = cb; c0 < mlim; c0 += kOutCols) {
                 const size_t o0 = (size_t)(m0 + c0 + tk) * ld + n;
                 const size_t step = (size_t)kTok * ld;
                 uint2 res[kIts];
@@ -584,26 +613,30 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                         if (c0 + tk + i * kTok < mlim) res[i] = *reinterpret_cast<const uint2*>(p.residual + o0 + i * step);
                 }
                 float acc[kOutCols];
-                if (w.partial) {
-                    // the contributors' partial tiles in order, two at a time in flight
-                    const float* src = part0 + (size_t)c0 * 128;
-#pragma unroll
-                    for (int j = 0; j < kOutCols; ++j) acc[j] = __ldcg(src + j * 128);
-#pragma unroll 1
-                    for (int q = 1; q < w.count; ++q) {
-                        src += part_step;
-                        float v[kOutCols];
-#pragma unroll
-                        for (int j = 0; j < kOutCols; ++j) v[j] = __ldcg(src + j * 128);
-#pragma unroll
-                        for (int j = 0; j < kOutCols; ++j) acc[j] += v[j];
-                    }
-                } else {
+                {
                     uint32_t r[kOutCols];
-                    tmem_ld_32x32b_x16(d + (uint32_t)c0, r);
+                    tmem_ld_32x32b_x8(d + (uint32_t)c0, r);
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < kOutCols; ++j) acc[j] = __uint_as_float(r[j]);
+                }
+                if (w.partial) {
+                    float own[kOutCols];
+#pragma unroll
+                    for (int j = 0; j < kOutCols; ++j) {
+                        own[j] = acc[j];
+                        acc[j] = w.index == 0 ? own[j] : x0[j];
+                        acc[j] += w.index == 0 ? x0[j] : w.index == 1 ? own[j] : x1[j];
+                        if (w.count > 2 && w.index <= 1) acc[j] += x1[j];
+                    }
+                    fetch(c0 + kOutCols);
+#pragma unroll 1
+                    for (int q = 2; q < w.count; ++q) {
+                        if (q == 2 && w.index <= 1) continue;  // added above
+#pragma unroll
+                        for (int j = 0; j < kOutCols; ++j)
+                            acc[j] += q == w.index ? own[j] : __ldcg(part0 + q * part_step + (size_t)(c0 + j) * 128);
+                    }
                 }
                 __syncwarp();  // the previous columns have left the buffer
 #pragma unroll
@@ -657,11 +690,9 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 }
                 put(p.y, v);
             }
-            if (!w.partial) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(cluster_map(&dempty[buf], 0));
-            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(cluster_map(&dempty[buf], 0));
         }
         if (!ok && lane == 0) fail();
     }
@@ -685,17 +716,22 @@ FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms) {
     g.tiles_c = (rows + 255) / 256;
     g.tiles = (int64_t)g.tiles_c * ((M + g.bn - 1) / g.bn);
     const int rest = (int)(g.tiles % g.pairs);
-    // Cycles of the last round and the cut tiles: a stage takes the longer of its MMAs and its dequant;
-    // joining a contributor's partial tile (512 bn bytes per CTA, written and read once) about 4 bn + 800,
-    // and 3000 for the count.  The rest alone may be cut (n runs per tile, at most one per pair), or the
-    // rest and one full round (one run per pair), which levels the pairs when the rest is small.
+    // Cycles that the last round and the cut tiles add: a stage takes the longer of its MMAs and its
+    // dequant; joining c contributors about (30 bn + 800) c + 3000, which hides behind the whole tiles
+    // that follow the cut ones, if there are any.  Either the rest alone is cut (n runs per tile, at most
+    // one per pair), or the rest and one full round (one run per pair).
     const double stage = std::max(1.45 * g.bn + 130.0, 440.0), tile = 2.0 * entries * stage;
+    auto join = [&](int c, bool hidden) {
+        const double cost = (30.0 * g.bn + 800.0) * c + 3000.0;
+        return hidden ? std::max(0.0, cost - tile) : cost;
+    };
     double best = rest > 0 ? tile : 0.0;
     for (int n = 2; rest > 0 && n <= 16; ++n) {
         const int runs = std::min(g.pairs, rest * n);
         const int units = rest * entries;
         if (units / runs < 2) break;
-        const double cost = 2.0 * stage * units / runs + (4.0 * g.bn + 800.0) * n + 3000.0;
+        const int c = runs % rest == 0 ? runs / rest : runs / rest + 2;  // most contributors of a tile
+        const double cost = 2.0 * stage * units / runs + join(c, g.tiles > g.pairs);
         if (cost < best) {
             best = cost;
             g.cut = rest;
@@ -703,8 +739,7 @@ FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms) {
         }
     }
     if (rest > 0 && g.tiles > g.pairs) {
-        const double share = (double)(rest + g.pairs) / g.pairs;  // tiles per pair
-        const double cost = (share - 1.0) * tile + (4.0 * g.bn + 800.0) * 3 + 3000.0;
+        const double cost = tile * rest / g.pairs + join(3, g.tiles > 2 * g.pairs);
         if (cost < best) {
             g.cut = rest + g.pairs;
             g.runs = g.pairs;
