@@ -1008,7 +1008,7 @@ w4a16_status awq_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint
     st = device_info(&d);
     if (st != W4A16_OK) return st;
     return from_cuda(launch_rmsnorm(x, residual, weight, s, eps, h, y, nullptr, nullptr, 0, M, (int)K, d->num_sms,
-                                    static_cast<cudaStream_t>(stream)));
+                                    d->status, static_cast<cudaStream_t>(stream)));
 }
 
 w4a16_status awq_rmsnorm_e4m3(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
@@ -1025,7 +1025,7 @@ w4a16_status awq_rmsnorm_e4m3(const uint16_t* x, const uint16_t* residual, const
     st = device_info(&d);
     if (st != W4A16_OK) return st;
     return from_cuda(launch_rmsnorm(x, residual, weight, s, eps, h, nullptr, q, scales, (int)group_size, M, (int)K,
-                                    d->num_sms, static_cast<cudaStream_t>(stream)));
+                                    d->num_sms, d->status, static_cast<cudaStream_t>(stream)));
 }
 
 w4a16_status awq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* weight, const float* s,
@@ -1043,7 +1043,7 @@ w4a16_status awq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const u
                  : device_info(&d);
     if (st != W4A16_OK) return st;
     return from_cuda(launch_rmsnorm_backward(dy, h, weight, s, dh, eps, dx, dweight, reinterpret_cast<float*>(ws), M,
-                                             (int)K, d->num_sms, static_cast<cudaStream_t>(stream)));
+                                             (int)K, d->num_sms, d->status, static_cast<cudaStream_t>(stream)));
 }
 
 w4a16_status w4a16_selftest_quotient(uint64_t* mismatches, uint32_t first[4], void* stream) {

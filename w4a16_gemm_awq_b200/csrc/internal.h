@@ -167,13 +167,13 @@ cudaError_t launch_gemm(const GemmMaps& maps, const GemmPlan& plan, int group_ra
 // y = bf16(v) (q == nullptr), or q and scales per `group` channels (y == nullptr); see rmsnorm.cu.
 cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
                            float eps, uint16_t* h, uint16_t* y, uint8_t* q, float* scales, int group, int64_t M, int K,
-                           int num_sms, cudaStream_t stream);
+                           int num_sms, unsigned* err, cudaStream_t stream);
 
 // partials: rmsnorm_backward_rows x K fp32, used with dweight.
 int rmsnorm_backward_rows(int64_t M, int K, int num_sms);
 cudaError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* weight, const float* s,
                                     const uint16_t* dh, float eps, uint16_t* dx, float* dweight, float* partials,
-                                    int64_t M, int K, int num_sms, cudaStream_t stream);
+                                    int64_t M, int K, int num_sms, unsigned* err, cudaStream_t stream);
 
 // The packed weights of a layer (w4a16_weights by value).
 struct PackedWeights {

@@ -6,12 +6,15 @@
 //   backward: xhat = h rstd;  w = dy weight / s;  dx = dh + rstd (w - xhat mean(w xhat));
 //             dweight = sum over rows of dy xhat / s
 //
-// Memory bound: a row sits in registers (8 channels per thread and chunk), so every input is read
-// once and every output written once; sums are fp32.  Many rows: 4 chunks per thread, so that a block
-// has up to 8 independent 16-byte loads per thread in flight and several rows share an SM; each block
-// walks rows and keeps weight / s in registers.  Few rows: as many threads per row as it has chunks,
-// which shortens the one row's latency.  The backward pass runs several rows per block side by side
-// (one group of warps each, with its own barrier) so that few partial sums of dweight are left.
+// Memory bound: every input is read once and every output written once; sums are fp32.
+//   - Many rows: a block walks rows that bulk copies bring into a ring in shared memory, so the loads of
+//     the next rows are in flight whatever the threads do with the current one (loads issued by the
+//     threads themselves, one row at a time: e4m3 1999 x 5120 26.6 us, backward 4096 x 4096 38.8 us;
+//     with the ring R1 and R2).  A thread holds 4 chunks of 8 channels of the row, packed as bf16 (the
+//     sum h is exact there), and weight / s.
+//   - Few rows: one block per row with as many threads as it has chunks, which shortens its latency.
+//   - The backward pass runs several rows per block side by side (one group of warps each, with its own
+//     ring and barrier), so that few partial sums of dweight are left.
 #include "common.cuh"
 #include "internal.h"
 
@@ -35,6 +38,8 @@ struct NormArgs {
     int group;                 // channels per scale
     long long M;
     int K;
+    int depth;                 // rows in the ring (many rows)
+    unsigned* err;
 };
 
 struct NormBwdArgs {
@@ -48,7 +53,11 @@ struct NormBwdArgs {
     float* partials;   // [gridDim.x][K] sums of dy xhat / s, or nullptr
     long long M;
     int K;
+    int depth;         // rows in a group's ring (many rows)
+    unsigned* err;
 };
+
+constexpr int kMaxDepth = 4;
 
 __device__ __forceinline__ void unpack8(const uint4& v, float f[8]) {
 #pragma unroll
@@ -108,87 +117,124 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// V: chunks of 8 channels per thread.  MAXT: most threads.  Q8: the e4m3 output.
-template <int V, int MAXT, bool Q8>
+// Waits for a row of the ring.  A thread whose wait runs out records it and goes on without waiting (on
+// what lies in the ring), since the others may already be at a barrier.
+__device__ __forceinline__ void row_wait(uint64_t* bar, uint32_t phase, bool& dead, unsigned* err) {
+    if (!dead && !mbar_wait_bounded(bar, phase)) {
+        dead = true;
+        record_error(err, kErrTimeout);
+    }
+}
+
+// max(m, |v|) with NaN above everything.
+__device__ __forceinline__ float max_abs_nan(float m, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_add(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// V: chunks of 8 channels per thread.  MAXT: most threads.  Q8: the e4m3 output.  RING: rows come through
+// the ring of bulk copies.  FULL: every thread has all its V chunks (K = 8 V T).
+//
+// The e4m3 output needs no second pass for the maximum: rstd is the same for the whole row, so with
+// u = h weight / s and G = max |u| of a group, scale = rstd G / 448 and v / scale = u (448 / G); G is
+// taken together with the sum of squares.
+template <int V, int MAXT, bool Q8, bool RING, bool FULL>
 __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const NormArgs p) {
     constexpr bool kKeep = V * MAXT <= 2048;  // weight / s stay in registers
     __shared__ float buf[2][1][32];
-    __shared__ uint32_t amax[2][Q8 ? 256 : 1];  // per group of a row, as bits of |v|: NaN > inf > finite
+    __shared__ uint32_t gmax[2][Q8 ? 256 : 1];  // per group of a row, as bits of |u|: NaN > inf > finite
+    __shared__ __align__(8) uint64_t full[kMaxDepth];
+    extern __shared__ __align__(128) uint16_t ring[];  // [depth][x row, residual row]
     const int T = blockDim.x, t = threadIdx.x, K = p.K;
-    float ws[kKeep ? V : 1][8];
-    if constexpr (kKeep) {
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-            const int k = (c * T + t) * 8;
-            if (k < K) load_ws(p.weight, p.s, k, ws[c]);
+    const bool add = p.residual != nullptr;
+    const int srcs = add ? 2 : 1;
+    // Thread 0 brings row m into slot `slot`.  Its earlier contents have been read: a barrier lies between.
+    auto load_row = [&](int slot, long long m) {
+        mbar_arrive_expect_tx(&full[slot], (uint32_t)(2 * K * srcs));
+        uint16_t* dst = ring + (size_t)slot * srcs * K;
+        bulk_load(dst, p.x + (size_t)m * K, (uint32_t)(2 * K), &full[slot]);
+        if (add) bulk_load(dst + K, p.residual + (size_t)m * K, (uint32_t)(2 * K), &full[slot]);
+    };
+    if constexpr (RING) {
+        if (t == 0) {
+            for (int i = 0; i < p.depth; ++i) mbar_init(&full[i], 1);
+            fence_mbarrier_init();
+            for (int i = 0; i < p.depth; ++i) {
+                const long long m = blockIdx.x + (long long)i * gridDim.x;
+                if (m < p.M) load_row(i, m);
+            }
         }
+        __syncthreads();
     }
+    float ws[kKeep ? V : 1][8];
+    int group[V];       // the scale that a chunk belongs to, and whether it writes it
+    bool first[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+        const int k = (c * T + t) * 8;
+        if (kKeep && (FULL || k < K)) load_ws(p.weight, p.s, k, ws[c]);
+        group[c] = Q8 ? k / p.group : 0;
+        first[c] = Q8 && k == group[c] * p.group;
+    }
+    auto weight_of = [&](int c, int k, float w[8]) {
+        if constexpr (kKeep) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = ws[c][e];
+        } else {
+            load_ws(p.weight, p.s, k, w);
+        }
+    };
     const int groups = Q8 ? K / p.group : 0;
     const bool shared_max = Q8 && p.group != 128;  // a group of 128 is 16 lanes of one warp
     if (shared_max) {
-        for (int i = t; i < groups; i += T) amax[0][i] = 0u;
+        for (int i = t; i < groups; i += T) gmax[0][i] = 0u;
         __syncthreads();
     }
-    int flip = 0;
+    const float inv_k = 1.0f / (float)K;
+    int flip = 0, slot = 0;
+    uint32_t phase = 0;
+    bool dead = false;
     for (long long m = blockIdx.x; m < p.M; m += gridDim.x, flip ^= 1) {
         const size_t row = (size_t)m * K;
+        const uint16_t* src = RING ? ring + (size_t)slot * srcs * K : p.x + row;
+        const uint16_t* src2 = RING ? src + K : p.residual + row;
+        if constexpr (RING) row_wait(&full[slot], phase, dead, p.err);
         uint4 a[V], r[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) {
             const int k = (c * T + t) * 8;
-            if (k < K) {
-                a[c] = __ldcs(reinterpret_cast<const uint4*>(p.x + row + k));
-                if (p.residual != nullptr) r[c] = __ldcs(reinterpret_cast<const uint4*>(p.residual + row + k));
+            if (FULL || k < K) {
+                a[c] = RING ? *reinterpret_cast<const uint4*>(src + k) : __ldcs(reinterpret_cast<const uint4*>(src + k));
+                if (add)
+                    r[c] = RING ? *reinterpret_cast<const uint4*>(src2 + k) : __ldcs(reinterpret_cast<const uint4*>(src2 + k));
             }
         }
-        // the row as rounded to bf16 stays packed in a: h is exact there, and the norm is that of h
+        // the row stays packed in a: h is exact there (the bf16 addition rounds the exact sum once), and
+        // the norm is that of h
         float ss[1] = {0.0f};
+        float lane_max[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) {
             const int k = (c * T + t) * 8;
-            if (k < K) {
-                float f[8];
-                unpack8(a[c], f);
-                if (p.residual != nullptr) {
-                    float g[8];
-                    unpack8(r[c], g);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] += g[e];
-                    a[c] = pack8(f);
-                    unpack8(a[c], f);
-                }
+            lane_max[c] = 0.0f;
+            if (FULL || k < K) {
+                if (add)
+                    a[c] = make_uint4(bf16x2_add(a[c].x, r[c].x), bf16x2_add(a[c].y, r[c].y), bf16x2_add(a[c].z, r[c].z),
+                                      bf16x2_add(a[c].w, r[c].w));
                 if (p.h != nullptr) *reinterpret_cast<uint4*>(p.h + row + k) = a[c];
+                float f[8], w[8];
+                unpack8(a[c], f);
+                if constexpr (Q8) weight_of(c, k, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss[0] = fmaf(f[e], f[e], ss[0]);
-            }
-        }
-        group_sum<1>(ss, buf[flip], t, T, 1);
-        const float rstd = rsqrtf(ss[0] / (float)K + p.eps);
-        auto scaled = [&](int c, int k, float f[8]) {  // v of chunk c
-            float w[8];
-            if constexpr (kKeep) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = ws[c][e];
-            } else {
-                load_ws(p.weight, p.s, k, w);
-            }
-            unpack8(a[c], f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * w[e];
-        };
-        uint32_t lane_max[V];
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-            const int k = (c * T + t) * 8;
-            lane_max[c] = 0u;
-            if (k < K) {
-                float f[8];
-                scaled(c, k, f);
-                if constexpr (Q8) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) lane_max[c] = max(lane_max[c], __float_as_uint(f[e]) & 0x7FFFFFFFu);
-                } else {
-                    *reinterpret_cast<uint4*>(p.y + row + k) = pack8(f);
+                for (int e = 0; e < 8; ++e) {
+                    ss[0] = fmaf(f[e], f[e], ss[0]);
+                    if constexpr (Q8) lane_max[c] = max_abs_nan(lane_max[c], f[e] * w[e]);
                 }
             }
         }
@@ -196,86 +242,140 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const NormArgs p) {
 #pragma unroll
             for (int c = 0; c < V; ++c) {
                 // 16 lanes hold 128 channels, all of one group
+                uint32_t u = __float_as_uint(lane_max[c]);
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) lane_max[c] = max(lane_max[c], __shfl_xor_sync(0xffffffffu, lane_max[c], o));
-                const int k = (c * T + t) * 8;
-                if (shared_max && (t & 15) == 0 && k < K) atomicMax(&amax[flip][k / p.group], lane_max[c]);
+                for (int o = 8; o > 0; o >>= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, o));
+                lane_max[c] = __uint_as_float(u);
+                if (shared_max && (t & 15) == 0 && (FULL || (c * T + t) * 8 < K)) atomicMax(&gmax[flip][group[c]], u);
             }
+        }
+        group_sum<1>(ss, buf[flip], t, T, 1);
+        if constexpr (RING) {  // every thread has its part of the row: the slot takes the row `depth` further on
+            const long long next = m + (long long)p.depth * gridDim.x;
+            if (t == 0 && next < p.M) load_row(slot, next);
+            if (++slot == p.depth) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+        const float rstd = rsqrtf(fmaf(ss[0], inv_k, p.eps));
+        if constexpr (Q8) {
             if (shared_max) {
-                __syncthreads();
+                __syncthreads();  // all maxima are in (one warp: group_sum has no barrier)
                 // the other buffer: read last in the previous row, used next in the next one
-                for (int i = t; i < groups; i += T) amax[flip ^ 1][i] = 0u;
+                for (int i = t; i < groups; i += T) gmax[flip ^ 1][i] = 0u;
             }
+        }
 #pragma unroll
-            for (int c = 0; c < V; ++c) {
-                const int k = (c * T + t) * 8;
-                if (k < K) {
-                    const int g = k / p.group;
-                    const float am = __uint_as_float(shared_max ? amax[flip][g] : lane_max[c]);
-                    const float sc = (am < kTiny ? kTiny : am) / kE4m3Max;
-                    const float inv = 1.0f / sc;
-                    float f[8];
-                    scaled(c, k, f);
-                    uint32_t w[2];
+        for (int c = 0; c < V; ++c) {
+            const int k = (c * T + t) * 8;
+            if (FULL || k < K) {
+                float f[8], w[8];
+                unpack8(a[c], f);
+                weight_of(c, k, w);
+                if constexpr (Q8) {
+                    const float g = shared_max ? __uint_as_float(gmax[flip][group[c]]) : lane_max[c];
+                    const float am = g * rstd;  // max |v|
+                    float sc = am / kE4m3Max, mul = kE4m3Max / g;
+                    if (!(am >= kTiny)) {  // below the least maximum, or a NaN, which spoils the whole group
+                        sc = am < kTiny ? kTiny / kE4m3Max : am;
+                        mul = am < kTiny ? rstd * (kE4m3Max / kTiny) : am;
+                    }
+                    uint32_t q[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        w[i] = e4m3x2(f[4 * i] * inv, f[4 * i + 1] * inv) |
-                               (e4m3x2(f[4 * i + 2] * inv, f[4 * i + 3] * inv) << 16);
-                    *reinterpret_cast<uint2*>(p.q + row + k) = make_uint2(w[0], w[1]);
-                    if (k % p.group == 0) p.scales[(size_t)m * groups + g] = sc;
+                        q[i] = e4m3x2(f[4 * i] * w[4 * i] * mul, f[4 * i + 1] * w[4 * i + 1] * mul) |
+                               (e4m3x2(f[4 * i + 2] * w[4 * i + 2] * mul, f[4 * i + 3] * w[4 * i + 3] * mul) << 16);
+                    *reinterpret_cast<uint2*>(p.q + row + k) = make_uint2(q[0], q[1]);
+                    if (first[c]) p.scales[(size_t)m * groups + group[c]] = sc;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * w[e];
+                    *reinterpret_cast<uint4*>(p.y + row + k) = pack8(f);
                 }
             }
+        }
+        if constexpr (Q8) {
             if (shared_max) __syncthreads();  // the cleared maxima are seen before the next row's
         }
     }
 }
 
-// A block holds blockDim.x / T groups of T threads, each on a row of its own.
-template <int V, int MAXT>
+// A block holds blockDim.x / T groups of T threads, each on a row of its own.  With c = rstd^3 sum(v h) / K
+// the gradient is dx = dh + rstd v - c h, and dweight's terms are rstd (dy h) / s.
+template <int V, int MAXT, bool RING, bool FULL>
 __global__ void __launch_bounds__(MAXT) rmsnorm_backward_kernel(const NormBwdArgs p, int T) {
     constexpr bool kKeep = V * MAXT <= 2048;
     constexpr int kGroups = 8;
     __shared__ float buf[kGroups][2][2][32];
-    extern __shared__ float4 part[];  // [groups - 1][K] sums of the other groups, when there are several
+    __shared__ __align__(8) uint64_t full[kGroups][kMaxDepth];
+    // RING: [group][depth][dy row, h row, dh row]; at the end [groups - 1][K] sums of the other groups
+    extern __shared__ __align__(128) uint8_t dyn[];
+    float4* part = reinterpret_cast<float4*>(dyn);
     const int K = p.K, grp = threadIdx.x / T, t = threadIdx.x - grp * T, groups = blockDim.x / T;
+    const bool stream = p.dh != nullptr;
+    const int srcs = stream ? 3 : 2;
+    const long long step = (long long)gridDim.x * groups;
+    uint16_t* ring = reinterpret_cast<uint16_t*>(dyn) + (size_t)grp * p.depth * srcs * K;
+    auto load_row = [&](int slot, long long m) {  // thread 0 of the group; the slot's earlier row has been read
+        mbar_arrive_expect_tx(&full[grp][slot], (uint32_t)(2 * K * srcs));
+        uint16_t* dst = ring + (size_t)slot * srcs * K;
+        bulk_load(dst, p.dy + (size_t)m * K, (uint32_t)(2 * K), &full[grp][slot]);
+        bulk_load(dst + K, p.h + (size_t)m * K, (uint32_t)(2 * K), &full[grp][slot]);
+        if (stream) bulk_load(dst + 2 * K, p.dh + (size_t)m * K, (uint32_t)(2 * K), &full[grp][slot]);
+    };
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sums' kernel waits for this one's end
+    if constexpr (RING) {
+        if (t == 0) {
+            for (int i = 0; i < p.depth; ++i) mbar_init(&full[grp][i], 1);
+            fence_mbarrier_init();
+            for (int i = 0; i < p.depth; ++i) {
+                const long long m = (long long)blockIdx.x * groups + grp + i * step;
+                if (m < p.M) load_row(i, m);
+            }
+        }
+        __syncthreads();
+    }
     float dw[V][8], ws[kKeep ? V : 1][8];
 #pragma unroll
     for (int c = 0; c < V; ++c) {
         const int k = (c * T + t) * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[c][e] = 0.0f;
-        if constexpr (kKeep) {
-            if (k < K) load_ws(p.weight, p.s, k, ws[c]);
-        }
+        if (kKeep && (FULL || k < K)) load_ws(p.weight, p.s, k, ws[c]);
     }
-    int flip = 0;
-    const long long step = (long long)gridDim.x * groups;
+    auto weight_of = [&](int c, int k, float w[8]) {
+        if constexpr (kKeep) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = ws[c][e];
+        } else {
+            load_ws(p.weight, p.s, k, w);
+        }
+    };
+    const float inv_k = 1.0f / (float)K;
+    int flip = 0, slot = 0;
+    uint32_t phase = 0;
+    bool dead = false;
     for (long long m = (long long)blockIdx.x * groups + grp; m < p.M; m += step, flip ^= 1) {
         const size_t row = (size_t)m * K;
-        uint4 g[V], hv[V], d4[V];
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-            const int k = (c * T + t) * 8;
-            if (k < K) {
-                g[c] = __ldcs(reinterpret_cast<const uint4*>(p.dy + row + k));
-                hv[c] = __ldcs(reinterpret_cast<const uint4*>(p.h + row + k));
-                if (p.dh != nullptr) d4[c] = __ldcs(reinterpret_cast<const uint4*>(p.dh + row + k));
-            }
-        }
+        const uint16_t* src = ring + (size_t)slot * srcs * K;
+        if constexpr (RING) row_wait(&full[grp][slot], phase, dead, p.err);
+        // The ring's rows are read twice from shared memory instead of being kept: three rows, the weights
+        // and the sums do not fit in the registers together.
+        uint4 g[RING ? 1 : V], hv[RING ? 1 : V];
         float s[2] = {0.0f, 0.0f};  // h^2, v h
 #pragma unroll
         for (int c = 0; c < V; ++c) {
             const int k = (c * T + t) * 8;
-            if (k < K) {
+            if (FULL || k < K) {
+                uint4& gc = g[RING ? 0 : c];
+                uint4& hc = hv[RING ? 0 : c];
+                gc = RING ? *reinterpret_cast<const uint4*>(src + k) : __ldcs(reinterpret_cast<const uint4*>(p.dy + row + k));
+                hc = RING ? *reinterpret_cast<const uint4*>(src + K + k) : __ldcs(reinterpret_cast<const uint4*>(p.h + row + k));
                 float a[8], h[8], w[8];
-                unpack8(g[c], a);
-                unpack8(hv[c], h);
-                if constexpr (kKeep) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = ws[c][e];
-                } else {
-                    load_ws(p.weight, p.s, k, w);
-                }
+                unpack8(gc, a);
+                unpack8(hc, h);
+                weight_of(c, k, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     s[0] = fmaf(h[e], h[e], s[0]);
@@ -284,43 +384,50 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_backward_kernel(const NormBwdArg
             }
         }
         group_sum<2>(s, buf[grp][flip], t, T, 1 + grp);
-        const float rstd = rsqrtf(s[0] / (float)K + p.eps);
-        const float mean = s[1] * rstd / (float)K;  // mean of v xhat
+        if constexpr (RING) {
+            // every thread has come past the previous row: its slot takes the row `depth` further on
+            const long long next = m + (long long)(p.depth - 1) * step;
+            if (t == 0 && m >= step && next < p.M) load_row(slot == 0 ? p.depth - 1 : slot - 1, next);
+        }
+        const float rstd = rsqrtf(fmaf(s[0], inv_k, p.eps));
+        const float c2 = -(rstd * rstd) * (rstd * (s[1] * inv_k));
 #pragma unroll
         for (int c = 0; c < V; ++c) {
             const int k = (c * T + t) * 8;
-            if (k < K) {
+            if (FULL || k < K) {
                 float a[8], h[8], w[8], d[8];
-                unpack8(g[c], a);
-                unpack8(hv[c], h);
-                if constexpr (kKeep) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = ws[c][e];
-                } else {
-                    load_ws(p.weight, p.s, k, w);
-                }
-                if (p.dh != nullptr) {
-                    unpack8(d4[c], d);
+                unpack8(RING ? *reinterpret_cast<const uint4*>(src + k) : g[RING ? 0 : c], a);
+                unpack8(RING ? *reinterpret_cast<const uint4*>(src + K + k) : hv[RING ? 0 : c], h);
+                if (stream) {
+                    unpack8(RING ? *reinterpret_cast<const uint4*>(src + 2 * K + k)
+                                 : __ldcs(reinterpret_cast<const uint4*>(p.dh + row + k)), d);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) d[e] = 0.0f;
                 }
+                weight_of(c, k, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float xh = h[e] * rstd;
-                    dw[c][e] = fmaf(a[e], xh, dw[c][e]);
-                    d[e] = fmaf(rstd, a[e] * w[e] - xh * mean, d[e]);
+                    dw[c][e] = fmaf(rstd, a[e] * h[e], dw[c][e]);
+                    d[e] = fmaf(c2, h[e], fmaf(rstd, a[e] * w[e], d[e]));
                 }
                 *reinterpret_cast<uint4*>(p.dx + row + k) = pack8(d);
+            }
+        }
+        if constexpr (RING) {
+            if (++slot == p.depth) {
+                slot = 0;
+                phase ^= 1;
             }
         }
     }
     if (p.partials == nullptr) return;
     // the groups' sums in group order, then one row of partials per block
+    __syncthreads();  // the rings are done: their memory takes the sums
 #pragma unroll
     for (int c = 0; c < V; ++c) {
         const int k = (c * T + t) * 8;
-        if (k < K && grp > 0) {
+        if ((FULL || k < K) && grp > 0) {
             float4* dst = part + ((size_t)(grp - 1) * K + k) / 4;
             dst[0] = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
             dst[1] = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
@@ -331,7 +438,7 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_backward_kernel(const NormBwdArg
 #pragma unroll
     for (int c = 0; c < V; ++c) {
         const int k = (c * T + t) * 8;
-        if (k < K) {
+        if (FULL || k < K) {
             float4 a = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
             float4 b = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
             for (int q = 0; q < groups - 1; ++q) {
@@ -353,6 +460,7 @@ __global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* parti
     __shared__ float part[8][32];
     const int lane = threadIdx.x & 31, rt = threadIdx.x >> 5;
     const int k = blockIdx.x * 32 + lane;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are complete
     float a = 0.0f;
     if (k < K) {
 #pragma unroll 8
@@ -371,63 +479,111 @@ int up32(int v) { return (v + 31) / 32 * 32; }
 // Threads per row for V chunks each.
 int norm_threads(int K, int V) { return up32((K + 8 * V - 1) / (8 * V)); }
 
-// Many rows: more than the SMs hold with one row each and 1024 threads per row.
+// Many rows: enough that each SM walks several.
 bool norm_many(int64_t M, int num_sms) { return M > 2 * num_sms; }
 
-template <bool Q8>
-void norm_launch(const NormArgs& a, int num_sms, cudaStream_t stream) {
-    const bool many = norm_many(a.M, num_sms);
-    const int V = many || a.K > 16384 ? 4 : a.K > 8192 ? 2 : 1;
-    const int T = norm_threads(a.K, V);
-    const int64_t cap = (int64_t)num_sms * (1024 / T > 1 ? 1024 / T : 1);
-    const int grid = (int)(a.M < cap || !many ? a.M : cap);
-    if (V == 1) rmsnorm_kernel<1, 1024, Q8><<<grid, T, 0, stream>>>(a);
-    else if (V == 2) rmsnorm_kernel<2, 1024, Q8><<<grid, T, 0, stream>>>(a);
-    else if (T <= 256) rmsnorm_kernel<4, 256, Q8><<<grid, T, 0, stream>>>(a);
-    else if (T <= 512) rmsnorm_kernel<4, 512, Q8><<<grid, T, 0, stream>>>(a);
-    else rmsnorm_kernel<4, 1024, Q8><<<grid, T, 0, stream>>>(a);
-}
+constexpr size_t kRingBytes = 200 * 1024;  // ring memory of an SM
 
-// The backward launch: chunks and threads per row, rows side by side per block, blocks.
-struct NormBwdPlan {
-    int V, T, groups, grid;
+// Forward launch.
+struct NormPlan {
+    int V, T, grid, depth;
+    size_t smem;
 };
 
-NormBwdPlan norm_backward_plan(int64_t M, int K, int num_sms) {
-    NormBwdPlan b;
+NormPlan norm_plan(int64_t M, int K, int srcs, int num_sms) {
+    NormPlan b{};
     const bool many = norm_many(M, num_sms);
     b.V = many || K > 16384 ? 4 : K > 8192 ? 2 : 1;
     b.T = norm_threads(K, b.V);
-    b.groups = many && b.T <= 256 ? (512 / b.T < 4 ? 512 / b.T : 4) : 1;
+    b.grid = (int)(M < (int64_t)num_sms * 65536 ? M : (int64_t)num_sms * 65536);
+    if (!many) return b;
+    // resident blocks by threads (at up to 112 registers each), then the ring's depth by shared memory
+    int blocks = 576 / b.T < 1 ? 1 : 576 / b.T > 8 ? 8 : 576 / b.T;
+    const size_t row = (size_t)2 * K * srcs;
+    while (blocks > 1 && (size_t)blocks * 2 * row > kRingBytes) --blocks;
+    b.depth = (int)(kRingBytes / blocks / row);
+    b.depth = b.depth < 1 ? 1 : b.depth > kMaxDepth ? kMaxDepth : b.depth;
+    b.smem = b.depth * row;
+    const int64_t cap = (int64_t)num_sms * blocks;
+    b.grid = (int)(M < cap ? M : cap);
+    return b;
+}
+
+template <int V, int MAXT, bool Q8, bool RING>
+cudaError_t norm_launch(const NormArgs& a, const NormPlan& b, cudaStream_t stream) {
+    auto* fn = a.K == 8 * V * b.T ? rmsnorm_kernel<V, MAXT, Q8, RING, true> : rmsnorm_kernel<V, MAXT, Q8, RING, false>;
+    if (b.smem > 32 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)b.smem);
+        if (e != cudaSuccess) return e;
+    }
+    fn<<<b.grid, b.T, b.smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool Q8>
+cudaError_t norm_dispatch(const NormArgs& a, const NormPlan& b, cudaStream_t stream) {
+    if (b.depth > 0) {
+        if (b.T <= 256) return norm_launch<4, 256, Q8, true>(a, b, stream);
+        if (b.T <= 512) return norm_launch<4, 512, Q8, true>(a, b, stream);
+        return norm_launch<4, 1024, Q8, true>(a, b, stream);
+    }
+    if (b.V == 1) return norm_launch<1, 1024, Q8, false>(a, b, stream);
+    if (b.V == 2) return norm_launch<2, 1024, Q8, false>(a, b, stream);
+    return norm_launch<4, 1024, Q8, false>(a, b, stream);
+}
+
+// The backward launch: chunks and threads per row, rows side by side per block, blocks, ring.
+struct NormBwdPlan {
+    int V, T, groups, grid, depth;
+    size_t smem;
+};
+
+NormBwdPlan norm_backward_plan(int64_t M, int K, int srcs, int num_sms) {
+    NormBwdPlan b{};
+    const bool many = norm_many(M, num_sms);
+    b.V = many || K > 16384 ? 4 : K > 8192 ? 2 : 1;
+    b.T = norm_threads(K, b.V);
+    b.groups = many && b.T <= 256 ? (512 / b.T < 8 ? 512 / b.T : 8) : 1;
     const int64_t need = (M + b.groups - 1) / b.groups;
     b.grid = (int)(need < num_sms ? need : num_sms);
+    if (!many) return b;
+    const size_t row = (size_t)2 * K * srcs;
+    // at least two rows: one is filled while the other is read
+    while (b.groups > 1 && 2 * b.groups * row > kRingBytes) --b.groups;
+    b.depth = (int)(kRingBytes / b.groups / row);
+    b.depth = b.depth > kMaxDepth ? kMaxDepth : b.depth;
+    if (b.depth < 2) b.depth = 0;  // rows too long: the threads load them themselves
+    b.smem = b.groups * b.depth * row;
     return b;
 }
 
 }  // namespace
 
-int rmsnorm_backward_rows(int64_t M, int K, int num_sms) { return norm_backward_plan(M, K, num_sms).grid; }
+int rmsnorm_backward_rows(int64_t M, int K, int num_sms) { return norm_backward_plan(M, K, 3, num_sms).grid; }
 
 cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
                            float eps, uint16_t* h, uint16_t* y, uint8_t* q, float* scales, int group, int64_t M, int K,
-                           int num_sms, cudaStream_t stream) {
-    const NormArgs a{x, residual, weight, s, eps, h, y, q, scales, group, M, K};
-    if (q != nullptr) norm_launch<true>(a, num_sms, stream);
-    else norm_launch<false>(a, num_sms, stream);
-    return cudaGetLastError();
+                           int num_sms, unsigned* err, cudaStream_t stream) {
+    const NormPlan b = norm_plan(M, K, residual != nullptr ? 2 : 1, num_sms);
+    const NormArgs a{x, residual, weight, s, eps, h, y, q, scales, group, M, K, b.depth, err};
+    return q != nullptr ? norm_dispatch<true>(a, b, stream) : norm_dispatch<false>(a, b, stream);
 }
 
 cudaError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* weight, const float* s,
                                     const uint16_t* dh, float eps, uint16_t* dx, float* dweight, float* partials,
-                                    int64_t M, int K, int num_sms, cudaStream_t stream) {
-    const NormBwdArgs a{dy, h, weight, s, dh, eps, dx, dweight != nullptr ? partials : nullptr, M, K};
-    const NormBwdPlan b = norm_backward_plan(M, K, num_sms);
+                                    int64_t M, int K, int num_sms, unsigned* err, cudaStream_t stream) {
+    const NormBwdPlan b = norm_backward_plan(M, K, dh != nullptr ? 3 : 2, num_sms);
+    const NormBwdArgs a{dy, h, weight, s, dh, eps, dx, dweight != nullptr ? partials : nullptr, M, K, b.depth, err};
     const int threads = b.T * b.groups;
-    const size_t smem = (size_t)(b.groups - 1) * K * 4;
-    auto* fn = b.V == 1 ? rmsnorm_backward_kernel<1, 1024>
-               : b.V == 2 ? rmsnorm_backward_kernel<2, 1024>
-               : threads <= 512 ? rmsnorm_backward_kernel<4, 512>
-                                : rmsnorm_backward_kernel<4, 1024>;
+    const size_t sums = (size_t)(b.groups - 1) * K * 4;
+    const size_t smem = b.smem > sums ? b.smem : sums;
+    const bool exact = K == 8 * b.V * b.T;
+    auto* fn = b.depth > 0 ? (threads > 512 ? rmsnorm_backward_kernel<4, 1024, true, false>
+                              : exact       ? rmsnorm_backward_kernel<4, 512, true, true>
+                                            : rmsnorm_backward_kernel<4, 512, true, false>)
+               : b.V == 1  ? rmsnorm_backward_kernel<1, 1024, false, false>
+               : b.V == 2  ? rmsnorm_backward_kernel<2, 1024, false, false>
+                           : rmsnorm_backward_kernel<4, 1024, false, false>;
     cudaError_t e;
     if (smem > 32 * 1024) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -436,8 +592,17 @@ cudaError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const
     fn<<<b.grid, threads, smem, stream>>>(a, b.T);
     e = cudaGetLastError();
     if (e != cudaSuccess || dweight == nullptr) return e;
-    rmsnorm_dweight_kernel<<<(K + 31) / 32, 256, 0, stream>>>(partials, s, dweight, b.grid, K);
-    return cudaGetLastError();
+    // the sums' kernel is scheduled while the rows are still walked and waits for their end
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((K + 31) / 32, 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rmsnorm_dweight_kernel, (const float*)partials, s, dweight, b.grid, K);
 }
 
 }  // namespace w4a16
