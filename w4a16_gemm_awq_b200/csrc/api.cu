@@ -381,6 +381,29 @@ FfnPlan plan_of(int op, int64_t M, int64_t N, int64_t K, int num_sms) {
     }
 }
 
+// Workspace of the feed-forward operators.  Decode: the counter region and the GEMV's partial tiles.
+// Otherwise the counter region, then
+//   the product's fp32 partial tiles;
+//   the tokens' scales [M] fp32 and the fp16 operand, not for LINEAR: x [M][K] forward, dp [M][N]
+//   backward (gated: dg and du);
+//   linear backward: the partial column sums of dbias.
+// For the norm's backward pass the partial sums of dweight follow the counters.
+struct FusedLayout {
+    size_t row_scale, operand, operand_bytes, sums, total;  // offsets after the counters
+};
+
+FusedLayout fused_layout(int op, int64_t M, int64_t N, int64_t K, int num_sms) {
+    FusedLayout L{};
+    const bool back = op == W4A16_OP_LINEAR_BACKWARD || op == W4A16_OP_GATED_BACKWARD;
+    L.row_scale = L.total = up256(plan_of(op, M, N, K, num_sms).partial_bytes);
+    if (op == W4A16_OP_LINEAR) return L;
+    L.operand = L.row_scale + up256((size_t)M * 4);
+    L.operand_bytes = up256((size_t)M * (size_t)(back ? N : K) * 2);
+    L.sums = L.operand + L.operand_bytes * (op == W4A16_OP_GATED_BACKWARD ? 2 : 1);
+    L.total = L.sums + (op == W4A16_OP_LINEAR_BACKWARD ? up256((size_t)linear_dp_runs(M, (int)N, num_sms) * N * 4) : 0);
+    return L;
+}
+
 // Whether an operator's forward product runs the decode GEMV (rows: output channels, 2 F gated).
 bool decodes(int op, int64_t M, int64_t N, int64_t K, int num_sms) {
     if ((op != W4A16_OP_LINEAR && op != W4A16_OP_GATED) || M > 16 || K > gemv_max_k()) return false;
@@ -388,20 +411,11 @@ bool decodes(int op, int64_t M, int64_t N, int64_t K, int num_sms) {
     return gemv_fits((int)rows, (int)K, num_sms);
 }
 
-// Workspace of the feed-forward operators: the counter region, then the product's fp32 partial
-// tiles; for the backward passes then dp [M][N] bf16 (gated: dg and du), then the partial column
-// sums of dbias.  For the norm's backward pass the partial sums of dweight follow the counters.
-size_t backward_dp_bytes(int64_t M, int64_t N) { return up256((size_t)M * (size_t)N * 2); }
-
 size_t fused_bytes(int op, int64_t M, int64_t N, int64_t K, int num_sms) {
     if (op == W4A16_OP_RMSNORM_BACKWARD)
         return kCounterRegionBytes + up256((size_t)rmsnorm_backward_rows(M, (int)K, num_sms) * K * 4);
     if (decodes(op, M, N, K, num_sms)) return kCounterRegionBytes + gemv_partial_bytes(num_sms);
-    const size_t b = kCounterRegionBytes + up256(plan_of(op, M, N, K, num_sms).partial_bytes);
-    if (op == W4A16_OP_LINEAR_BACKWARD)
-        return b + backward_dp_bytes(M, N) + up256((size_t)linear_dp_blocks(M) * N * 4);
-    if (op == W4A16_OP_GATED_BACKWARD) return b + 2 * backward_dp_bytes(M, N);
-    return b;
+    return kCounterRegionBytes + fused_layout(op, M, N, K, num_sms).total;
 }
 
 // Checks the caller's workspace against fused_bytes and returns its part after the counters.
@@ -416,13 +430,14 @@ w4a16_status take_fused_workspace(int op, int64_t M, int64_t N, int64_t K, void*
     return W4A16_OK;
 }
 
-// Tensor map of row-major bf16 activations [rows][cols] in boxes of 64 columns x box_rows.
-w4a16_status encode_rows(EncodeTiledFn enc, CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t cols, int box_rows) {
+// Tensor map of row-major 16-bit activations [rows][cols] in boxes of 64 columns x box_rows.
+w4a16_status encode_rows(EncodeTiledFn enc, CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t cols, int box_rows,
+                         CUtensorMapDataType type) {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p), dims, strides, box, estr,
+    return enc(map, type, 2, const_cast<uint16_t*>(p), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? W4A16_OK
@@ -471,19 +486,31 @@ w4a16_status run_ffn_decode(int op, const FfnArgs& a, const DeviceInfo& d, void*
 }
 
 // The product of a feed-forward operator; ws: the workspace after its counters.
-w4a16_status run_ffn(int op, const FfnArgs& a, const DeviceInfo& d, void* workspace, uint8_t* ws, cudaStream_t stream) {
+w4a16_status run_ffn(int op, const FfnArgs& args, const DeviceInfo& d, void* workspace, uint8_t* ws,
+                     cudaStream_t stream) {
     const bool back = op == W4A16_OP_LINEAR_BACKWARD || op == W4A16_OP_GATED_BACKWARD;
     const bool two = op == W4A16_OP_GATED || op == W4A16_OP_GATED_BACKWARD;
-    if (decodes(op, a.M, a.N, a.K, d.num_sms)) return run_ffn_decode(op, a, d, workspace, ws, stream);
+    if (decodes(op, args.M, args.N, args.K, d.num_sms)) return run_ffn_decode(op, args, d, workspace, ws, stream);
+    FfnArgs a = args;
     const FfnPlan plan = plan_of(op, a.M, a.N, a.K, d.num_sms);
     if (plan.tiles > INT_MAX / 2) return W4A16_ERR_UNSUPPORTED;  // 32-bit tile indexes
     EncodeTiledFn enc = nullptr;
     w4a16_status st = encoder(&enc);
     if (st != W4A16_OK) return st;
+    if (op == W4A16_OP_GATED) {
+        const FusedLayout L = fused_layout(op, a.M, a.N, a.K, d.num_sms);
+        float* row_scale = reinterpret_cast<float*>(ws + L.row_scale);
+        uint16_t* xh = reinterpret_cast<uint16_t*>(ws + L.operand);
+        st = from_cuda(launch_half_rows(a.a, xh, row_scale, a.M, a.K, d.num_sms, stream));
+        if (st != W4A16_OK) return st;
+        a.a = xh;
+        a.row_scale = row_scale;
+    }
     FfnMaps maps;
-    st = encode_rows(enc, &maps.x, a.a, a.M, back ? a.N : a.K, plan.bn / 2);
+    const CUtensorMapDataType type = op == W4A16_OP_LINEAR ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    st = encode_rows(enc, &maps.x, a.a, a.M, back ? a.N : a.K, plan.bn / 2, type);
     maps.x2 = maps.x;
-    if (st == W4A16_OK && a.a2 != nullptr) st = encode_rows(enc, &maps.x2, a.a2, a.M, a.N, plan.bn / 2);
+    if (st == W4A16_OK && a.a2 != nullptr) st = encode_rows(enc, &maps.x2, a.a2, a.M, a.N, plan.bn / 2, type);
     if (st == W4A16_OK) st = encode_packed(enc, &maps.w, a.w.qweight, a.N, a.K);
     maps.w2 = maps.w;
     if (st == W4A16_OK && two) st = encode_packed(enc, &maps.w2, a.w2.qweight, a.N, a.K);
@@ -915,16 +942,14 @@ w4a16_status w4a16_linear_fused_backward(const uint16_t* dy, const uint16_t* pre
     st = take_fused_workspace(W4A16_OP_LINEAR_BACKWARD, M, N, K, workspace, workspace_bytes, &d, &ws);
     if (st != W4A16_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool act = activation != W4A16_ACT_NONE;
-    uint8_t* grads = ws + up256(plan_of(W4A16_OP_LINEAR_BACKWARD, M, N, K, d->num_sms).partial_bytes);
-    uint16_t* dp = act ? reinterpret_cast<uint16_t*>(grads) : nullptr;
-    float* sums = reinterpret_cast<float*>(grads + backward_dp_bytes(M, N));
-    if (act || dbias) {
-        st = from_cuda(launch_linear_dp(dy, pre, dp, dbias, sums, static_cast<unsigned*>(workspace), M, (int)N, activation,
-                                        s));
-        if (st != W4A16_OK) return st;
-    }
-    a.a = act ? dp : dy;
+    const FusedLayout L = fused_layout(W4A16_OP_LINEAR_BACKWARD, M, N, K, d->num_sms);
+    float* row_scale = reinterpret_cast<float*>(ws + L.row_scale);
+    uint16_t* dp = reinterpret_cast<uint16_t*>(ws + L.operand);
+    st = from_cuda(launch_linear_dp(dy, pre, dp, row_scale, dbias, reinterpret_cast<float*>(ws + L.sums),
+                                    static_cast<unsigned*>(workspace), M, (int)N, activation, d->num_sms, s));
+    if (st != W4A16_OK) return st;
+    a.a = dp;
+    a.row_scale = row_scale;
     a.y = dx;
     a.M = M;
     a.N = (int)N;
@@ -981,11 +1006,13 @@ w4a16_status w4a16_gated_backward(const uint16_t* dh, const uint16_t* g, const u
     st = take_fused_workspace(W4A16_OP_GATED_BACKWARD, M, F, K, workspace, workspace_bytes, &d, &ws);
     if (st != W4A16_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint8_t* grads = ws + up256(plan_of(W4A16_OP_GATED_BACKWARD, M, F, K, d->num_sms).partial_bytes);
-    uint16_t* dg = reinterpret_cast<uint16_t*>(grads);
-    uint16_t* du = reinterpret_cast<uint16_t*>(grads + backward_dp_bytes(M, F));
-    st = from_cuda(launch_gated_dp(dh, g, u, dg, du, M, (int)F, activation, d->num_sms, s));
+    const FusedLayout L = fused_layout(W4A16_OP_GATED_BACKWARD, M, F, K, d->num_sms);
+    float* row_scale = reinterpret_cast<float*>(ws + L.row_scale);
+    uint16_t* dg = reinterpret_cast<uint16_t*>(ws + L.operand);
+    uint16_t* du = reinterpret_cast<uint16_t*>(ws + L.operand + L.operand_bytes);
+    st = from_cuda(launch_gated_dp(dh, g, u, dg, du, row_scale, M, (int)F, activation, d->num_sms, d->status, s));
     if (st != W4A16_OK) return st;
+    a.row_scale = row_scale;
     a.a = dg;
     a.a2 = du;
     a.y = dx;

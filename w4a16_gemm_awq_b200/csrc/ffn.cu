@@ -1,11 +1,16 @@
-// ffn.cu -- the elementwise steps of the feed-forward operators' backward passes: the gradient before
-// the activation, rounded to bf16 as the product's operand, and the bias gradient from the unrounded
-// values.
+// ffn.cu -- the activations of the feed-forward products as their kernel takes them, and the elementwise
+// steps of the backward passes.
 //
-// Memory bound: 16-byte loads and stores, every element read and written once.  The bias sums are
-// taken in the same pass: a block covers 256 columns x a run of rows and leaves its fp32 column sums
-// in the workspace; the last block of a column range to arrive (a counter, reset to zero) adds them in
-// the order of the runs, so no second launch is needed and the bits do not depend on which is last.
+// The products' operand is fp16 with a scale per token: x' = fp16(x 2^-e), e such that the token's
+// largest |x'| lies in [2^14, 2^15) (backward: the largest |dy| in [2^13, 2^14), and |act'| <= 1.13).
+// bf16 values keep all their 8 bits down to 2^-28 of the token's largest one, and below that an error
+// of at most 2^-39 of it is left, under the fp32 sums' own; gradients are rounded to 11 bits.
+//
+// Memory bound: 16-byte loads and stores, each row read from device memory once (a second pass over a
+// row comes from the caches).  The bias sums are taken in the same pass as the gradients: a block covers
+// 256 columns x a run of rows and leaves its fp32 column sums in the workspace; the last block of a
+// column range to arrive (a counter, reset to zero) adds them in the order of the runs, so no second
+// launch is needed and the bits do not depend on which is last.
 #include "act.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -15,7 +20,7 @@ namespace w4a16 {
 namespace {
 
 constexpr int kDpCols = 256;  // columns per block: 32 threads x 8
-constexpr int kDpRowThreads = 8;
+constexpr int kDpRowThreads = 16;
 
 __device__ __forceinline__ void unpack8(const uint4& v, float f[8]) {
 #pragma unroll
@@ -26,25 +31,95 @@ __device__ __forceinline__ void unpack8(const uint4& v, float f[8]) {
     }
 }
 
-__device__ __forceinline__ uint4 pack8(const float f[8]) {
+__device__ __forceinline__ uint4 pack8_half(const float f[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        const __half2 b = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// dp = dy * act'(pre) over `rows` rows per block; dp nullptr: only the bias sums are wanted (no
-// activation).  sums: [gridDim.y][N], nullptr without a bias gradient.
+// e for a token whose largest magnitude has the fp32 bits `bits`: over 2^e it lies in [2^top, 2^(top+1)).
+// e is kept in the range of the normal numbers.  With an infinity or a NaN in the token, e is that of the
+// largest finite value, so that no finite one becomes infinite beside it.
+__device__ __forceinline__ int token_exponent(uint32_t bits, int top) {
+    const int E = (int)(bits >> 23);
+    if (bits == 0u) return 0;
+    return max(min(E, 254) - 127 - top, -110);
+}
+
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ uint32_t max_abs8(const uint4& v, uint32_t m) {  // of packed bf16, as bf16 bits in both halves
+    m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
+    m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
+    m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
+    return __vmaxu2(m, v.w & 0x7FFF7FFFu);
+}
+
+// The block's largest value; buf: 32 words.
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* buf) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int l = threadIdx.x & 31;
+    v = __reduce_max_sync(0xffffffffu, l < (int)(blockDim.x >> 5) ? buf[l] : 0u);
+    __syncthreads();  // buf may be used again
+    return v;
+}
+
+// One block per row: row_scale[m] = 2^e, and out = fp16(x 2^-e) unless out is nullptr.
+__global__ void __launch_bounds__(256) half_rows_kernel(const uint16_t* x, uint16_t* out, float* row_scale, long long M,
+                                                        int K, int top) {
+    __shared__ uint32_t buf[32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
+    constexpr int V = 4;  // chunks of a row that stay in registers
+    for (long long m = blockIdx.x; m < M; m += gridDim.x) {
+        const uint16_t* row = x + m * K;
+        uint4 a[V];
+        uint32_t mx = 0u;
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int k = (c * 256 + threadIdx.x) * 8;
+            if (k < K) {
+                a[c] = *reinterpret_cast<const uint4*>(row + k);
+                mx = max_abs8(a[c], mx);
+            }
+        }
+        for (int k = (V * 256 + threadIdx.x) * 8; k < K; k += 2048) mx = max_abs8(*reinterpret_cast<const uint4*>(row + k), mx);
+        mx = block_max(max(mx & 0xFFFFu, mx >> 16), buf);
+        const int e = token_exponent(mx << 16, top);
+        if (threadIdx.x == 0) row_scale[m] = exp2_int(e);
+        if (out == nullptr) continue;
+        const float s = exp2_int(-e);
+        auto put = [&](const uint4& v, int k) {
+            float f[8];
+            unpack8(v, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= s;
+            *reinterpret_cast<uint4*>(out + m * K + k) = pack8_half(f);
+        };
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int k = (c * 256 + threadIdx.x) * 8;
+            if (k < K) put(a[c], k);
+        }
+        for (int k = (V * 256 + threadIdx.x) * 8; k < K; k += 2048) put(*reinterpret_cast<const uint4*>(row + k), k);
+    }
+}
+
+// dp = fp16(dy * act'(pre) / row_scale) over `rows` rows per block.  sums: [gridDim.y][N], nullptr without
+// a bias gradient.
 template <int ACT>
 __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_kernel(const uint16_t* dy, const uint16_t* pre,
-                                                                       uint16_t* dp, float* sums, float* dbias,
-                                                                       unsigned* counters, long long M, int N, int rows) {
+                                                                       uint16_t* dp, const float* row_scale,
+                                                                       float* sums, float* dbias, unsigned* counters, long long M, int N, int rows) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
     __shared__ float part[kDpRowThreads][kDpCols];
     __shared__ int last;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' scales come from the kernel before
     const int lane = threadIdx.x & 31, rt = threadIdx.x >> 5;
     const int n = blockIdx.x * kDpCols + lane * 8;
     const bool in = n < N;
@@ -60,25 +135,29 @@ __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_kernel(const uin
                 unpack8(__ldcs(reinterpret_cast<const uint4*>(pre + m * N + n)), p);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] *= act_grad<ACT>(p[e]);
-                *reinterpret_cast<uint4*>(dp + m * N + n) = pack8(v);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) a[e] += v[e];
+            const float s = 1.0f / row_scale[m];  // a power of two: exact
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= s;
+            *reinterpret_cast<uint4*>(dp + m * N + n) = pack8_half(v);
         }
     }
     if (sums == nullptr) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) part[rt][lane * 8 + e] = a[e];
     __syncthreads();
-    const int c = threadIdx.x, nc = blockIdx.x * kDpCols + c;  // one column per thread
+    const int c = threadIdx.x & (kDpCols - 1), nc = blockIdx.x * kDpCols + c;  // one column per thread
+    const bool mine = threadIdx.x < kDpCols && nc < N;
     float s = 0.0f;
 #pragma unroll
     for (int r = 0; r < kDpRowThreads; ++r) s += part[r][c];
     if (gridDim.y == 1) {
-        if (nc < N) dbias[nc] = s;
+        if (mine) dbias[nc] = s;
         return;
     }
-    if (nc < N) __stcg(sums + (size_t)blockIdx.y * N + nc, s);
+    if (mine) __stcg(sums + (size_t)blockIdx.y * N + nc, s);
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -86,7 +165,7 @@ __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_kernel(const uin
         if (last) atomicExch(counters + blockIdx.x, 0u);
     }
     __syncthreads();
-    if (!last || nc >= N) return;
+    if (!last || !mine) return;
     __threadfence();
     s = 0.0f;
 #pragma unroll 8
@@ -94,61 +173,200 @@ __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_kernel(const uin
     dbias[nc] = s;
 }
 
-// dg = dh u act'(g), du = dh act(g); n: elements / 8.
-template <int ACT>
-__global__ void __launch_bounds__(256) gated_dp_kernel(const uint4* dh, const uint4* g, const uint4* u, uint4* dg,
-                                                       uint4* du, long long n) {
+constexpr int kDpDepth = 4;
+
+// dg = dh u act'(g), du = dh act(g), both in fp16 over the row's scale; one row per block at a time.  KEEP
+// (F <= 32 threads): rows come by bulk copies through a ring of `depth`, so that the next rows are on
+// their way while one is computed (a block's threads loading row by row took 76 us instead of DP us at
+// 2048 x 14336), and a row's values stay in registers between the maximum and the rounding.  Longer rows
+// are read and computed twice.
+template <int ACT, bool KEEP>
+__global__ void __launch_bounds__(512) gated_dp_kernel(const uint16_t* dh, const uint16_t* g, const uint16_t* u,
+                                                       uint16_t* dg, uint16_t* du, float* row_scale, long long M, int F,
+                                                       int depth, unsigned* err) {
+    constexpr int V = KEEP ? 4 : 1;
+    __shared__ uint32_t buf[32];
+    __shared__ __align__(8) uint64_t full[kDpDepth];
+    extern __shared__ __align__(128) uint16_t ring[];  // KEEP: [depth][dh row, g row, u row]
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-        float d[8], a[8], b[8], x[8], y[8];
-        unpack8(__ldcs(dh + i), d);
-        unpack8(__ldcs(g + i), a);
-        unpack8(__ldcs(u + i), b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = d[e] * b[e] * act_grad<ACT>(a[e]);
-            y[e] = d[e] * act_value<ACT>(a[e]);
+    const int T = blockDim.x;
+    auto load_row = [&](int slot, long long m) {  // thread 0; the slot's earlier row has been read
+        mbar_arrive_expect_tx(&full[slot], (uint32_t)(6 * F));
+        uint16_t* dst = ring + (size_t)slot * 3 * F;
+        bulk_load(dst, dh + (size_t)m * F, (uint32_t)(2 * F), &full[slot]);
+        bulk_load(dst + F, g + (size_t)m * F, (uint32_t)(2 * F), &full[slot]);
+        bulk_load(dst + 2 * F, u + (size_t)m * F, (uint32_t)(2 * F), &full[slot]);
+    };
+    if constexpr (KEEP) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < depth; ++i) mbar_init(&full[i], 1);
+            fence_mbarrier_init();
+            for (int i = 0; i < depth; ++i) {
+                const long long m = blockIdx.x + (long long)i * gridDim.x;
+                if (m < M) load_row(i, m);
+            }
         }
-        dg[i] = pack8(x);
-        du[i] = pack8(y);
+        __syncthreads();
+    }
+    int slot = 0;
+    uint32_t phase = 0;
+    bool dead = false;
+    for (long long m = blockIdx.x; m < M; m += gridDim.x) {
+        const size_t row = (size_t)m * F;
+        const uint16_t* s0 = KEEP ? ring + (size_t)slot * 3 * F : dh + row;
+        const uint16_t* s1 = KEEP ? s0 + F : g + row;
+        const uint16_t* s2 = KEEP ? s0 + 2 * F : u + row;
+        // a wait that runs out is recorded, and the thread goes on without waiting: the others may already be
+        // at a barrier
+        if (KEEP && !dead && !mbar_wait_bounded(&full[slot], phase)) {
+            dead = true;
+            record_error(err, kErrTimeout);
+        }
+        float x[V][8], y[V][8];
+        auto values = [&](int k, float (&xv)[8], float (&yv)[8]) {
+            float d[8], a[8], b[8];
+            unpack8(*reinterpret_cast<const uint4*>(s0 + k), d);
+            unpack8(*reinterpret_cast<const uint4*>(s1 + k), a);
+            unpack8(*reinterpret_cast<const uint4*>(s2 + k), b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xv[e] = d[e] * b[e] * act_grad<ACT>(a[e]);
+                yv[e] = d[e] * act_value<ACT>(a[e]);
+            }
+        };
+        uint32_t mx = 0u;
+        auto largest = [&](const float (&xv)[8], const float (&yv)[8]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                mx = max(mx, max(__float_as_uint(xv[e]) & 0x7FFFFFFFu, __float_as_uint(yv[e]) & 0x7FFFFFFFu));
+        };
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                const int k = (c * T + threadIdx.x) * 8;
+                if (k < F) {
+                    values(k, x[c], y[c]);
+                    largest(x[c], y[c]);
+                }
+            }
+        } else {
+            for (int k = threadIdx.x * 8; k < F; k += T * 8) {
+                values(k, x[0], y[0]);
+                largest(x[0], y[0]);
+            }
+        }
+        const int e = token_exponent(block_max(mx, buf), 14);
+        if constexpr (KEEP) {  // every thread has its part of the row
+            const long long next = m + (long long)depth * gridDim.x;
+            if (threadIdx.x == 0 && next < M) load_row(slot, next);
+            if (++slot == depth) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+        if (threadIdx.x == 0) row_scale[m] = exp2_int(e);
+        const float s = exp2_int(-e);
+        auto put = [&](int k, float (&xv)[8], float (&yv)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                xv[i] *= s;
+                yv[i] *= s;
+            }
+            *reinterpret_cast<uint4*>(dg + row + k) = pack8_half(xv);
+            *reinterpret_cast<uint4*>(du + row + k) = pack8_half(yv);
+        };
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                const int k = (c * T + threadIdx.x) * 8;
+                if (k < F) put(k, x[c], y[c]);
+            }
+        } else {
+            for (int k = threadIdx.x * 8; k < F; k += T * 8) {
+                values(k, x[0], y[0]);
+                put(k, x[0], y[0]);
+            }
+        }
     }
 }
 
 }  // namespace
 
-// Runs of rows: at least 16 rows each, and few enough that adding the runs up (N threads, one load per
-// run) stays short.  (64 runs at 1023 x 5120 took 20 us, most of it in the last blocks' sums.)
-int linear_dp_blocks(int64_t M) { return (int)((M + 15) / 16 < 32 ? (M + 15) / 16 : 32); }
+// Runs of rows: blocks for one round of two per SM, at least 16 rows each, and few enough that adding the
+// runs up (one load per run and column in the last block) stays short.  (64 runs at 1023 x 5120 took
+// 20 us, most of it in those sums.)
+int linear_dp_runs(int64_t M, int N, int num_sms) {
+    const int64_t cols = (N + kDpCols - 1) / kDpCols, most = (M + kDpRowThreads - 1) / kDpRowThreads;
+    const int64_t runs = 2 * num_sms / cols;
+    return (int)(runs < 1 ? 1 : runs > 32 ? (most < 32 ? most : 32) : runs > most ? most : runs);
+}
 
-cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* dbias, float* sums,
-                             unsigned* counters, int64_t M, int N, int act, cudaStream_t stream) {
-    const int runs = linear_dp_blocks(M);
-    const int rows = (int)((M + runs - 1) / runs);
-    const dim3 grid((N + kDpCols - 1) / kDpCols, (unsigned)((M + rows - 1) / rows));
-    float* s = dbias != nullptr ? sums : nullptr;
-#define W4A16_DP(ACT) \
-    case ACT: linear_dp_kernel<ACT><<<grid, 32 * kDpRowThreads, 0, stream>>>(dy, pre, dp, s, dbias, counters, M, N, rows); break
-    switch (act) {
-        W4A16_DP(W4A16_ACT_NONE);
-        W4A16_DP(W4A16_ACT_RELU);
-        W4A16_DP(W4A16_ACT_SILU);
-        W4A16_DP(W4A16_ACT_GELU);
-        W4A16_DP(W4A16_ACT_GELU_TANH);
-        default: return cudaErrorInvalidValue;
-    }
-#undef W4A16_DP
+namespace {
+
+int row_blocks(int64_t M, int num_sms) { return (int)(M < (int64_t)num_sms * 16 ? M : (int64_t)num_sms * 16); }
+
+template <typename... Args>
+cudaError_t launch_after(void (*fn)(Args...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_half_rows(const uint16_t* x, uint16_t* out, float* row_scale, int64_t M, int K, int num_sms,
+                             cudaStream_t stream) {
+    half_rows_kernel<<<row_blocks(M, num_sms), 256, 0, stream>>>(x, out, row_scale, M, K, 14);
     return cudaGetLastError();
 }
 
+cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* row_scale, float* dbias,
+                             float* sums, unsigned* counters, int64_t M, int N, int act, int num_sms,
+                             cudaStream_t stream) {
+    if (act == W4A16_ACT_NONE && dbias == nullptr) return launch_half_rows(dy, dp, row_scale, M, N, num_sms, stream);
+    half_rows_kernel<<<row_blocks(M, num_sms), 256, 0, stream>>>(dy, nullptr, row_scale, M, N, 13);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int runs = linear_dp_runs(M, N, num_sms);
+    const int rows = (int)((M + runs - 1) / runs);
+    const dim3 grid((N + kDpCols - 1) / kDpCols, (unsigned)((M + rows - 1) / rows));
+    float* s = dbias != nullptr ? sums : nullptr;
+    auto* fn = act == W4A16_ACT_NONE   ? linear_dp_kernel<W4A16_ACT_NONE>
+               : act == W4A16_ACT_RELU ? linear_dp_kernel<W4A16_ACT_RELU>
+               : act == W4A16_ACT_SILU ? linear_dp_kernel<W4A16_ACT_SILU>
+               : act == W4A16_ACT_GELU ? linear_dp_kernel<W4A16_ACT_GELU>
+                                       : linear_dp_kernel<W4A16_ACT_GELU_TANH>;
+    return launch_after(fn, grid, 32 * kDpRowThreads, stream, dy, pre, dp, (const float*)row_scale, s, dbias, counters,
+                        (long long)M, N, rows);
+}
+
 cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dg, uint16_t* du,
-                            int64_t M, int F, int act, int num_sms, cudaStream_t stream) {
-    const long long n = (long long)M * F / 8;
-    const long long blocks = (n + 255) / 256;
-    const int grid = (int)(blocks < (long long)num_sms * 8 ? blocks : (long long)num_sms * 8);
-    auto v = [](const uint16_t* p) { return reinterpret_cast<const uint4*>(p); };
-    auto w = [](uint16_t* p) { return reinterpret_cast<uint4*>(p); };
+                            float* row_scale, int64_t M, int F, int act, int num_sms, unsigned* err,
+                            cudaStream_t stream) {
+    const bool keep = F <= 16384;  // 512 threads with four chunks each
+    const int threads = keep ? (F / 32 + 31) / 32 * 32 : 512;
+    // resident blocks by registers (128 a thread at most), and at least two rows in flight for each
+    constexpr size_t kRing = 200 * 1024;
+    const size_t row = (size_t)6 * F;
+    int blocks = 512 / threads > 8 ? 8 : 512 / threads;
+    while (keep && blocks > 1 && 2 * blocks * row > kRing) --blocks;
+    int depth = keep ? (int)(kRing / blocks / row) : 0;
+    depth = depth > kDpDepth ? kDpDepth : depth;
+    const int64_t cap = (int64_t)num_sms * (keep ? blocks : 4);
+    const int grid = (int)(M < cap ? M : cap);
+    const size_t smem = (size_t)depth * row;
+    using Kernel = void (*)(const uint16_t*, const uint16_t*, const uint16_t*, uint16_t*, uint16_t*, float*, long long, int,
+                            int, unsigned*);
+    Kernel fn = nullptr;
 #define W4A16_DP(ACT) \
-    case ACT: gated_dp_kernel<ACT><<<grid, 256, 0, stream>>>(v(dh), v(g), v(u), w(dg), w(du), n); break
+    case ACT: fn = keep ? gated_dp_kernel<ACT, true> : gated_dp_kernel<ACT, false>; break
     switch (act) {
         W4A16_DP(W4A16_ACT_NONE);
         W4A16_DP(W4A16_ACT_RELU);
@@ -158,6 +376,11 @@ cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_
         default: return cudaErrorInvalidValue;
     }
 #undef W4A16_DP
+    if (smem > 32 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    fn<<<grid, threads, smem, stream>>>(dh, g, u, dg, du, row_scale, M, F, depth, err);
     return cudaGetLastError();
 }
 

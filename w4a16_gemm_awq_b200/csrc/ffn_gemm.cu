@@ -4,7 +4,13 @@
 //   LINEAR    y[m][n] = bf16( act( sum_k x[m][k] w[n][k] + bias[n] ) + residual[m][n] )
 //   GATED     h[m][f] = bf16( act( sum_k x[m][k] wg[f][k] ) * sum_k x[m][k] wu[f][k] )
 //   BACKWARD  dx[m][k] = bf16( sum_n dp[m][n] w[n][k] (+ sum_n dp2[m][n] w2[n][k]) )
-//   w = bf16((q - z) scale), rounded once.
+//   w = (q - z) scale, rounded once: to bf16 for LINEAR, whose activations are taken as they are, and to
+//   fp16 for the others, whose activations are fp16 scaled by a power of two per token (ffn.cu), which
+//   keeps every bit of theirs that fp32 sums can show; the epilogue undoes the scale.  The others have
+//   several rounded factors per output: with bf16 the relative 2-norm against 64 bits was 2.9e-3 for the
+//   gated output and for dx, where their own rounding to bf16 makes 1.7e-3; with fp16 it is 1.7e-3.
+//   LINEAR is at 2.3e-3, and a pass over x to convert it would cost up to a tenth of the call (2048
+//   tokens, K 14336: 18 us of 200).
 //
 // Design (B200):
 //   - A CTA pair computes a tile of 256 output channels x BN tokens (BN a multiple of 32 up to 256)
@@ -22,9 +28,11 @@
 //     in the layout that the MMA reads, conflict-free.  Forward products contract over k, so a packed
 //     row becomes a row of A (K-major).  The backward product contracts over n, so a packed row
 //     becomes a column of A: it is stored as it lies and the MMA reads A channel-major (MN-major).
-//   - One rounding per weight at two multiplications: with scale = hi + lo, hi = bf16(scale), lo has
-//     at most 3 bits and (q - z) 4, so (q - z) lo is exact in bf16 and fma(q - z, hi, (q - z) lo) is
-//     the correctly rounded product.
+//   - fp16: a packed word becomes 8 weights in 13 operations: nibble pairs 0 and 1 are masked in place
+//     into the mantissa of 1024 (as q and 16 q), 2 and 3 after one shift by 8; one subtraction or fused
+//     multiply-add gives q - z exactly, one multiplication by the scale rounds.  bf16 has no room for the
+//     second nibble and not for an fp16 scale: 19 operations, with scale = hi + lo, hi = bf16(scale); lo
+//     has at most 3 bits and q - z 4, so (q - z) lo is exact and fma(q - z, hi, (q - z) lo) rounds once.
 //   - GATED interleaves gate and up rows in sixteens, so the two sums of a channel sit in one warp's
 //     lanes l and l + 16 and meet by a shuffle.
 //   - Whole tiles go round the pairs; the tiles that do not fill a round are cut along the contraction
@@ -79,6 +87,7 @@ struct GemmArgs2 {
     float* partials;
     unsigned* counters;
     unsigned* err;
+    const float* row_scale;  // [M] what a token's sums are multiplied by (not for LINEAR)
     int M, N, K;       // N: rows of one weight matrix
     int gr;            // group size / 128
     int act;
@@ -178,9 +187,18 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         : "memory");
 }
 
-__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
-    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b),
-                                     *reinterpret_cast<__nv_bfloat162*>(&c));
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b), *reinterpret_cast<__half2*>(&c));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -192,30 +210,63 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// A row's scale and zero point in one group, as the dequant needs them.
-struct RowParams {
-    uint32_t hi, lo, zero;  // bf16 pairs: scale's leading part, its rest, 128 + z
+// w & MASK over the bits of MAGIC.
+template <uint32_t MASK, uint32_t MAGIC>
+__device__ __forceinline__ uint32_t mask_into(uint32_t w) {
+    uint32_t t;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(t) : "r"(w), "n"(MASK), "r"(MAGIC));
+    return t;
+}
+
+// A packed row's scale and zero point in one group, and the 8 weights of a packed word in element order.
+struct HalfRow {
+    uint32_t scale, low, high;  // pairs: scale; 1024 + z; -(64 + z)
+
+    __device__ __forceinline__ HalfRow(uint32_t s, uint32_t z)
+        : scale(s | (s << 16)), low(0x64006400u | z | (z << 16)), high((0xD400u | (z << 4)) * 0x10001u) {}
+
+    __device__ __forceinline__ uint4 operator()(uint32_t w) const {
+        const uint32_t w8 = w >> 8, sixteenth = 0x2C002C00u;
+        const uint32_t a = h2_sub(mask_into<0x000F000Fu, 0x64006400u>(w), low);
+        const uint32_t b = h2_fma(mask_into<0x00F000F0u, 0x64006400u>(w), sixteenth, high);
+        const uint32_t c = h2_sub(mask_into<0x000F000Fu, 0x64006400u>(w8), low);
+        const uint32_t d = h2_fma(mask_into<0x00F000F0u, 0x64006400u>(w8), sixteenth, high);
+        return make_uint4(h2_mul(a, scale), h2_mul(b, scale), h2_mul(c, scale), h2_mul(d, scale));
+    }
 };
 
-__device__ __forceinline__ RowParams row_params(uint16_t scale, uint32_t z) {
-    const float s = fp16_bits_to_float(scale);
-    const uint32_t hi = float_to_bf16_bits(s);
-    const uint32_t lo = float_to_bf16_bits(s - bf16_bits_to_float((uint16_t)hi));
-    return RowParams{hi | (hi << 16), lo | (lo << 16), 0x43004300u | z | (z << 16)};
-}
+struct Bf16Row {
+    uint32_t hi, lo, zero;  // pairs: the scale's leading part and its rest; 128 + z
 
-// The 8 weights of a packed word as bf16, in element order.
-__device__ __forceinline__ uint4 dequant_word(uint32_t word, const RowParams& r) {
-    uint32_t v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t t;
-        asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(t) : "r"(word >> (4 * i)), "r"(0x000F000Fu), "r"(0x43004300u));
-        t = bf16x2_sub(t, r.zero);
-        v[i] = bf16x2_fma(t, r.hi, bf16x2_mul(t, r.lo));
+    __device__ __forceinline__ Bf16Row(uint32_t s, uint32_t z) {
+        const float f = fp16_bits_to_float((uint16_t)s);
+        hi = float_to_bf16_bits(f);
+        lo = (uint32_t)float_to_bf16_bits(f - bf16_bits_to_float((uint16_t)hi)) * 0x10001u;
+        hi *= 0x10001u;
+        zero = 0x43004300u | z | (z << 16);
     }
-    return make_uint4(v[0], v[1], v[2], v[3]);
-}
+
+    __device__ __forceinline__ uint32_t pair(uint32_t w) const {
+        uint32_t t = bf16x2_sub(mask_into<0x000F000Fu, 0x43004300u>(w), zero);
+        uint32_t l = bf16x2_mul(t, lo);
+        const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&t), *reinterpret_cast<const __nv_bfloat162*>(&hi),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&l));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+
+    __device__ __forceinline__ uint4 operator()(uint32_t w) const {
+        return make_uint4(pair(w), pair(w >> 4), pair(w >> 8), pair(w >> 12));
+    }
+};
+
+template <int MODE>
+struct Dequant {
+    using Row = HalfRow;
+};
+template <>
+struct Dequant<kLinear> {
+    using Row = Bf16Row;
+};
 
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -407,8 +458,8 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issue
         if (rank == 0) {
-            // D fp32, A and B bf16, B K-major, A K-major or (backward) MN-major, M = 256, N = bn
-            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (MODE == kBackward ? 1u << 15 : 0u) |
+            // D fp32, A and B fp16 (LINEAR: bf16), B K-major, A K-major or (backward) MN-major, M = 256, N = bn
+            const uint32_t idesc = (1u << 4) | (MODE == kLinear ? 1u << 7 | 1u << 10 : 0u) | (MODE == kBackward ? 1u << 15 : 0u) |
                                    ((uint32_t)(p.bn >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
             const uint32_t base = smem_u32(smem);
             const uint64_t a0 = MODE == kBackward ? smem_desc(base + kAOff, 8192, 1024) : smem_desc(base + kAOff, 16, 1024);
@@ -494,7 +545,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         Packed cur{}, next{};
         if (group < stages) ok = fetch(group, cur);
         for (int s = group; ok && s < stages; s += kGroups) {
-            const RowParams rp = row_params((uint16_t)cur.scale, cur.zword & 15u);
+            const typename Dequant<MODE>::Row weights(cur.scale, cur.zword & 15u);
             if (s + kGroups < stages && !fetch(s + kGroups, next)) {
                 ok = false;
                 break;
@@ -508,7 +559,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
 #pragma unroll
             for (int c = 0; c < 8; ++c)
                 *reinterpret_cast<uint4*>(a + ((c << 4) ^ sw)) =
-                    dequant_word(c < 4 ? u4_get(cur.a, c) : u4_get(cur.b, c - 4), rp);
+                    weights(c < 4 ? u4_get(cur.a, c) : u4_get(cur.b, c - 4));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(cluster_map(&full[slot], 0));
@@ -585,8 +636,14 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             const int n = MODE == kGated ? tc * 128 + rank * 64 + 16 * quarter + ch : tc * 256 + rank * 128 + 32 * quarter + ch;
             const int ld = MODE == kBackward ? p.K : p.N;
             const bool in = n < ld;  // the last pair's second half may be past N (whole warps)
-            float bias = 0.0f;
-            if (MODE == kLinear && p.bias != nullptr && in) bias = bf16_bits_to_float(p.bias[n - ch + lane]);
+            float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (MODE == kLinear && p.bias != nullptr && in) {
+                const uint2 b = *reinterpret_cast<const uint2*>(p.bias + n);
+                bias[0] = __uint_as_float(b.x << 16);
+                bias[1] = __uint_as_float(b.x & 0xFFFF0000u);
+                bias[2] = __uint_as_float(b.y << 16);
+                bias[3] = __uint_as_float(b.y & 0xFFFF0000u);
+            }
             // the partial tiles of the first two other contributors, fetched one chunk ahead (those after them
             // are rare)
             float x0[kOutCols], x1[kOutCols];
@@ -606,6 +663,12 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             for (int c0 = cb; c0 < mlim; c0 += kOutCols) {
                 const size_t o0 = (size_t)(m0 + c0 + tk) * ld + n;
                 const size_t step = (size_t)kTok * ld;
+                float token[kIts];  // the tokens' scales
+#pragma unroll
+                for (int i = 0; i < kIts; ++i)
+                    token[i] = MODE == kLinear                ? 1.0f
+                               : c0 + tk + i * kTok < mlim ? __ldcg(p.row_scale + m0 + c0 + tk + i * kTok)
+                                                           : 0.0f;
                 uint2 res[kIts];
                 if (MODE == kLinear && p.residual != nullptr && in) {
 #pragma unroll
@@ -640,16 +703,16 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 }
                 __syncwarp();  // the previous columns have left the buffer
 #pragma unroll
-                for (int j = 0; j < kOutCols; ++j) out[j * kOutStride + lane] = acc[j] + bias;
+                for (int j = 0; j < kOutCols; ++j) out[j * kOutStride + lane] = acc[j];
                 __syncwarp();
                 float v[4 * kIts];
 #pragma unroll
                 for (int i = 0; i < kIts; ++i) {
                     const float4 a = *reinterpret_cast<const float4*>(out + (tk + i * kTok) * kOutStride + ch);
-                    v[4 * i] = a.x;
-                    v[4 * i + 1] = a.y;
-                    v[4 * i + 2] = a.z;
-                    v[4 * i + 3] = a.w;
+                    v[4 * i] = fmaf(a.x, token[i], bias[0]);
+                    v[4 * i + 1] = fmaf(a.y, token[i], bias[1]);
+                    v[4 * i + 2] = fmaf(a.z, token[i], bias[2]);
+                    v[4 * i + 3] = fmaf(a.w, token[i], bias[3]);
                 }
                 auto put = [&](uint16_t* dst, const float (&f)[4 * kIts]) {
 #pragma unroll
@@ -663,10 +726,10 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
 #pragma unroll
                     for (int i = 0; i < kIts; ++i) {
                         const float4 a = *reinterpret_cast<const float4*>(out + (tk + i * kTok) * kOutStride + 16 + ch);
-                        u[4 * i] = a.x;
-                        u[4 * i + 1] = a.y;
-                        u[4 * i + 2] = a.z;
-                        u[4 * i + 3] = a.w;
+                        u[4 * i] = a.x * token[i];
+                        u[4 * i + 1] = a.y * token[i];
+                        u[4 * i + 2] = a.z * token[i];
+                        u[4 * i + 3] = a.w * token[i];
                     }
                     if (p.pre != nullptr) {
                         put(p.pre, v);
@@ -762,6 +825,7 @@ cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnA
     g.partials = partials;
     g.counters = counters;
     g.err = err;
+    g.row_scale = a.row_scale;
     g.M = (int)a.M;
     g.N = a.N;
     g.K = a.K;

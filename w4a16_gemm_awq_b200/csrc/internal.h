@@ -182,11 +182,13 @@ struct PackedWeights {
     const uint32_t* zeros;
 };
 
-// A feed-forward product (see ffn_gemm.cu).  Forward: a = x [M][K], outputs [M][N].  Backward: a (and
-// a2) [M][N], output y [M][K].  w2, pre2 and a2 belong to the gated forms.
+// A feed-forward product.  Forward: a = x [M][K], outputs [M][N].  Backward: a (and a2) [M][N], output y
+// [M][K].  w2, pre2 and a2 belong to the gated forms.  The decode GEMV and the forward linear product take a
+// in bf16, the other tensor-core products in fp16 with row_scale [M] (see ffn.cu).
 struct FfnArgs {
     const uint16_t* a;
     const uint16_t* a2;
+    const float* row_scale;
     PackedWeights w, w2;
     const uint16_t* bias;
     const uint16_t* residual;
@@ -218,12 +220,18 @@ struct FfnMaps {
 cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnArgs& a, bool back, bool two,
                             float* partials, unsigned* counters, unsigned* err, cudaStream_t stream);
 
-// The elementwise steps of the backward passes.  sums: linear_dp_blocks(M) x N fp32, used with dbias.
-int linear_dp_blocks(int64_t M);
-// counters: one per 256 columns, zero between calls.
-cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* dbias, float* sums,
-                             unsigned* counters, int64_t M, int N, int act, cudaStream_t stream);
+// fp16 activations with a scale per token, as the tensor-core products take them (see ffn.cu).
+cudaError_t launch_half_rows(const uint16_t* x, uint16_t* out, float* row_scale, int64_t M, int K, int num_sms,
+                             cudaStream_t stream);
+
+// The gradients before the activation, in the same form.  sums: linear_dp_runs x N fp32, used with
+// dbias; counters: one per 256 columns, zero between calls.
+int linear_dp_runs(int64_t M, int N, int num_sms);
+cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* row_scale, float* dbias,
+                             float* sums, unsigned* counters, int64_t M, int N, int act, int num_sms,
+                             cudaStream_t stream);
 cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dg, uint16_t* du,
-                            int64_t M, int F, int act, int num_sms, cudaStream_t stream);
+                            float* row_scale, int64_t M, int F, int act, int num_sms, unsigned* err,
+                            cudaStream_t stream);
 
 }  // namespace w4a16
