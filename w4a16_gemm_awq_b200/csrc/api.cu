@@ -385,21 +385,20 @@ FfnPlan plan_of(int op, int64_t M, int64_t N, int64_t K, int num_sms) {
 // Otherwise the counter region, then
 //   the product's fp32 partial tiles;
 //   the tokens' scales [M] fp32 and the fp16 operand, not for LINEAR: x [M][K] forward, dp [M][N]
-//   backward (gated: dg and du);
+//   backward (gated: [M][2 N], dg beside du);
 //   linear backward: the partial column sums of dbias.
 // For the norm's backward pass the partial sums of dweight follow the counters.
 struct FusedLayout {
-    size_t row_scale, operand, operand_bytes, sums, total;  // offsets after the counters
+    size_t row_scale, operand, sums, total;  // offsets after the counters
 };
 
 FusedLayout fused_layout(int op, int64_t M, int64_t N, int64_t K, int num_sms) {
     FusedLayout L{};
-    const bool back = op == W4A16_OP_LINEAR_BACKWARD || op == W4A16_OP_GATED_BACKWARD;
     L.row_scale = L.total = up256(plan_of(op, M, N, K, num_sms).partial_bytes);
     if (op == W4A16_OP_LINEAR) return L;
+    const int64_t width = op == W4A16_OP_GATED ? K : op == W4A16_OP_LINEAR_BACKWARD ? N : 2 * N;
     L.operand = L.row_scale + up256((size_t)M * 4);
-    L.operand_bytes = up256((size_t)M * (size_t)(back ? N : K) * 2);
-    L.sums = L.operand + L.operand_bytes * (op == W4A16_OP_GATED_BACKWARD ? 2 : 1);
+    L.sums = L.operand + up256((size_t)M * (size_t)width * 2);
     L.total = L.sums + (op == W4A16_OP_LINEAR_BACKWARD ? up256((size_t)linear_dp_runs(M, (int)N, num_sms) * N * 4) : 0);
     return L;
 }
@@ -508,9 +507,7 @@ w4a16_status run_ffn(int op, const FfnArgs& args, const DeviceInfo& d, void* wor
     }
     FfnMaps maps;
     const CUtensorMapDataType type = op == W4A16_OP_LINEAR ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    st = encode_rows(enc, &maps.x, a.a, a.M, back ? a.N : a.K, plan.bn / 2, type);
-    maps.x2 = maps.x;
-    if (st == W4A16_OK && a.a2 != nullptr) st = encode_rows(enc, &maps.x2, a.a2, a.M, a.N, plan.bn / 2, type);
+    st = encode_rows(enc, &maps.x, a.a, a.M, !back ? a.K : two ? 2 * (int64_t)a.N : a.N, plan.bn / 2, type);
     if (st == W4A16_OK) st = encode_packed(enc, &maps.w, a.w.qweight, a.N, a.K);
     maps.w2 = maps.w;
     if (st == W4A16_OK && two) st = encode_packed(enc, &maps.w2, a.w2.qweight, a.N, a.K);
@@ -1008,13 +1005,11 @@ w4a16_status w4a16_gated_backward(const uint16_t* dh, const uint16_t* g, const u
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const FusedLayout L = fused_layout(W4A16_OP_GATED_BACKWARD, M, F, K, d->num_sms);
     float* row_scale = reinterpret_cast<float*>(ws + L.row_scale);
-    uint16_t* dg = reinterpret_cast<uint16_t*>(ws + L.operand);
-    uint16_t* du = reinterpret_cast<uint16_t*>(ws + L.operand + L.operand_bytes);
-    st = from_cuda(launch_gated_dp(dh, g, u, dg, du, row_scale, M, (int)F, activation, d->num_sms, d->status, s));
+    uint16_t* dp = reinterpret_cast<uint16_t*>(ws + L.operand);
+    st = from_cuda(launch_gated_dp(dh, g, u, dp, row_scale, M, (int)F, activation, d->num_sms, d->status, s));
     if (st != W4A16_OK) return st;
     a.row_scale = row_scale;
-    a.a = dg;
-    a.a2 = du;
+    a.a = dp;
     a.y = dx;
     a.M = M;
     a.N = (int)F;

@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(256) half_rows_kernel(const uint16_t* x, uint1
 template <int ACT>
 __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_kernel(const uint16_t* dy, const uint16_t* pre,
                                                                        uint16_t* dp, const float* row_scale,
-                                                                       float* sums, float* dbias, unsigned* counters, long long M, int N, int rows) {
+                                                                       float* sums, float* dbias, unsigned* counters,
+                                                                       long long M, int N, int rows) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
     __shared__ float part[kDpRowThreads][kDpCols];
     __shared__ int last;
@@ -175,15 +176,15 @@ __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_kernel(const uin
 
 constexpr int kDpDepth = 4;
 
-// dg = dh u act'(g), du = dh act(g), both in fp16 over the row's scale; one row per block at a time.  KEEP
-// (F <= 32 threads): rows come by bulk copies through a ring of `depth`, so that the next rows are on
-// their way while one is computed (a block's threads loading row by row took 76 us instead of DP us at
-// 2048 x 14336), and a row's values stay in registers between the maximum and the rounding.  Longer rows
-// are read and computed twice.
+// dg = dh u act'(g), du = dh act(g), both in fp16 over the row's scale, side by side in dp [M][2 F]; one
+// row per block at a time.  KEEP (F <= 32 threads): rows come by bulk copies through a ring of `depth`,
+// so that the next rows are on their way while one is computed (a block's threads loading row by row
+// took 76 us instead of 51 us at 2048 x 14336, 294 MB), and a row's values stay in registers between the
+// maximum and the rounding.  Longer rows are read and computed twice.
 template <int ACT, bool KEEP>
 __global__ void __launch_bounds__(512) gated_dp_kernel(const uint16_t* dh, const uint16_t* g, const uint16_t* u,
-                                                       uint16_t* dg, uint16_t* du, float* row_scale, long long M, int F,
-                                                       int depth, unsigned* err) {
+                                                       uint16_t* dp, float* row_scale, long long M, int F, int depth,
+                                                       unsigned* err) {
     constexpr int V = KEEP ? 4 : 1;
     __shared__ uint32_t buf[32];
     __shared__ __align__(8) uint64_t full[kDpDepth];
@@ -272,8 +273,8 @@ __global__ void __launch_bounds__(512) gated_dp_kernel(const uint16_t* dh, const
                 xv[i] *= s;
                 yv[i] *= s;
             }
-            *reinterpret_cast<uint4*>(dg + row + k) = pack8_half(xv);
-            *reinterpret_cast<uint4*>(du + row + k) = pack8_half(yv);
+            *reinterpret_cast<uint4*>(dp + 2 * row + k) = pack8_half(xv);
+            *reinterpret_cast<uint4*>(dp + 2 * row + F + k) = pack8_half(yv);
         };
         if constexpr (KEEP) {
 #pragma unroll
@@ -347,9 +348,8 @@ cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* 
                         (long long)M, N, rows);
 }
 
-cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dg, uint16_t* du,
-                            float* row_scale, int64_t M, int F, int act, int num_sms, unsigned* err,
-                            cudaStream_t stream) {
+cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dp, float* row_scale,
+                            int64_t M, int F, int act, int num_sms, unsigned* err, cudaStream_t stream) {
     const bool keep = F <= 16384;  // 512 threads with four chunks each
     const int threads = keep ? (F / 32 + 31) / 32 * 32 : 512;
     // resident blocks by registers (128 a thread at most), and at least two rows in flight for each
@@ -362,8 +362,8 @@ cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_
     const int64_t cap = (int64_t)num_sms * (keep ? blocks : 4);
     const int grid = (int)(M < cap ? M : cap);
     const size_t smem = (size_t)depth * row;
-    using Kernel = void (*)(const uint16_t*, const uint16_t*, const uint16_t*, uint16_t*, uint16_t*, float*, long long, int,
-                            int, unsigned*);
+    using Kernel = void (*)(const uint16_t*, const uint16_t*, const uint16_t*, uint16_t*, float*, long long, int, int,
+                            unsigned*);
     Kernel fn = nullptr;
 #define W4A16_DP(ACT) \
     case ACT: fn = keep ? gated_dp_kernel<ACT, true> : gated_dp_kernel<ACT, false>; break
@@ -380,7 +380,7 @@ cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_
         const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    fn<<<grid, threads, smem, stream>>>(dh, g, u, dg, du, row_scale, M, F, depth, err);
+    fn<<<grid, threads, smem, stream>>>(dh, g, u, dp, row_scale, M, F, depth, err);
     return cudaGetLastError();
 }
 

@@ -3,7 +3,7 @@
 //
 //   LINEAR    y[m][n] = bf16( act( sum_k x[m][k] w[n][k] + bias[n] ) + residual[m][n] )
 //   GATED     h[m][f] = bf16( act( sum_k x[m][k] wg[f][k] ) * sum_k x[m][k] wu[f][k] )
-//   BACKWARD  dx[m][k] = bf16( sum_n dp[m][n] w[n][k] (+ sum_n dp2[m][n] w2[n][k]) )
+//   BACKWARD  dx[m][k] = bf16( sum_n dp[m][n] w[n][k] (+ sum_n dp[m][N + n] w2[n][k]) )
 //   w = (q - z) scale, rounded once: to bf16 for LINEAR, whose activations are taken as they are, and to
 //   fp16 for the others, whose activations are fp16 scaled by a power of two per token (ffn.cu), which
 //   keeps every bit of theirs that fp32 sums can show; the epilogue undoes the scale.  The others have
@@ -57,6 +57,10 @@ constexpr int kEpilogue0 = 4, kDequant0 = 12;
 constexpr int kThreads = 32 * (kDequant0 + 4 * kGroups);
 constexpr int kS = 6;                    // stages of 64 contraction steps
 constexpr int kP = 3;                    // packed entries of 128 contraction steps
+// A wait by parity takes a phase for the one two before it.  So a dequant group that uses a slot uses it in
+// every phase: having waited for each phase in turn it can never pass on an old one, in whatever order the
+// copies land.
+static_assert(kS % kGroups == 0 && 2 * kP % kGroups == 0, "the groups meet their slots in every phase");
 constexpr int kABytes = 128 * 128;       // 128 channels x 64 steps, bf16
 constexpr int kBBytes = 128 * 128;       // up to 128 tokens (this CTA's half) x 64 steps, bf16
 constexpr int kEntryBytes = 128 * 64;    // 128 packed rows of 16 words
@@ -300,9 +304,8 @@ __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 2
 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
-ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_x2,
-                const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_w2,
-                const GemmArgs2 p) {
+ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                const __grid_constant__ CUtensorMap map_w2, const GemmArgs2 p) {
     // Pointers derive from the array itself, so that the compiler keeps the shared address space.
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {  // the swizzled stages need 1024-byte alignment
@@ -343,6 +346,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     }
     if (warp == 0) prefetch_tensormap(&map_x);
     if (warp == 2) prefetch_tensormap(&map_w);
+    if (warp == 2 && MODE != kLinear) prefetch_tensormap(&map_w2);
     if (warp == 3) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(kTmemCols) : "memory");
@@ -426,11 +430,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 }
                 if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)p.bn * 128u);
-                    uint8_t* dst = smem + kBOff + slot * kBBytes;
-                    if (MODE == kBackward && c >= 2 * p.entries1)
-                        tma_load_2d_pair(dst, &map_x2, cluster_map(&full[slot], 0), (c - 2 * p.entries1) * 64, m0);
-                    else
-                        tma_load_2d_pair(dst, &map_x, cluster_map(&full[slot], 0), c * 64, m0);
+                    tma_load_2d_pair(smem + kBOff + slot * kBBytes, &map_x, cluster_map(&full[slot], 0), c * 64, m0);
                 }
                 __syncwarp();
             }
@@ -853,7 +853,7 @@ cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnA
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, maps.x, maps.x2, maps.w, maps.w2, g);
+    return cudaLaunchKernelEx(&cfg, fn, maps.x, maps.w, maps.w2, g);
 }
 
 }  // namespace w4a16

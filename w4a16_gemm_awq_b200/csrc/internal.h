@@ -182,12 +182,11 @@ struct PackedWeights {
     const uint32_t* zeros;
 };
 
-// A feed-forward product.  Forward: a = x [M][K], outputs [M][N].  Backward: a (and a2) [M][N], output y
-// [M][K].  w2, pre2 and a2 belong to the gated forms.  The decode GEMV and the forward linear product take a
+// A feed-forward product.  Forward: a = x [M][K], outputs [M][N].  Backward: a [M][N] (gated: [M][2 N]),
+// output y [M][K].  w2 and pre2 belong to the gated forms.  The decode GEMV and the forward linear product take a
 // in bf16, the other tensor-core products in fp16 with row_scale [M] (see ffn.cu).
 struct FfnArgs {
     const uint16_t* a;
-    const uint16_t* a2;
     const float* row_scale;
     PackedWeights w, w2;
     const uint16_t* bias;
@@ -211,10 +210,10 @@ struct FfnPlan {
 };
 FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms);
 
-// Tensor maps: x, x2: the activations (dp, dp2 backward), boxes of 64 contraction steps x bn / 2 tokens,
-// 128-byte swizzle; w, w2: qweight [N][K/8], boxes of 16 words x 64 rows, 64-byte swizzle.
+// Tensor maps: x: the activations (dp backward), boxes of 64 contraction steps x bn / 2 tokens, 128-byte
+// swizzle; w, w2: qweight [N][K/8], boxes of 16 words x 64 rows, 64-byte swizzle.
 struct FfnMaps {
-    CUtensorMap x, x2, w, w2;
+    CUtensorMap x, w, w2;
 };
 // counters: 2 per cut tile, zero between calls.
 cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnArgs& a, bool back, bool two,
@@ -224,14 +223,14 @@ cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnA
 cudaError_t launch_half_rows(const uint16_t* x, uint16_t* out, float* row_scale, int64_t M, int K, int num_sms,
                              cudaStream_t stream);
 
-// The gradients before the activation, in the same form.  sums: linear_dp_runs x N fp32, used with
+// The gradients before the activation, in the same form (gated: dg and du side by side, [M][2 F]).  sums: linear_dp_runs x N fp32, used with
 // dbias; counters: one per 256 columns, zero between calls.
 int linear_dp_runs(int64_t M, int N, int num_sms);
 cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* row_scale, float* dbias,
                              float* sums, unsigned* counters, int64_t M, int N, int act, int num_sms,
                              cudaStream_t stream);
-cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dg, uint16_t* du,
-                            float* row_scale, int64_t M, int F, int act, int num_sms, unsigned* err,
+cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dp, float* row_scale,
+                            int64_t M, int F, int act, int num_sms, unsigned* err,
                             cudaStream_t stream);
 
 }  // namespace w4a16
