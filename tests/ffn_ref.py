@@ -1,16 +1,19 @@
 """64-bit reference of the feed-forward operators, and the error bounds of their kernels.
 
-Bounds (every rounding to bf16 is off by at most 2^-8 of the value):
+Bounds (every rounding to bf16 is off by at most 2^-8 of the value, to fp16 by 2^-11):
   projection, M <= 16  the decode GEMV's bound of parity.py (exact weights, fp32 sums);
-  projection, M > 16   2^-8 sum |x w| (each weight rounded once to bf16) + fp32 sums, whose chain is
-                       K / 16 adds in the tensor core and at most 64 outside, 2^-22 each;
+  projection, M > 16   linear: 2^-8 sum |x w| (each weight rounded once to bf16); gated: 2^-11 sum |x w|
+                       (weights rounded to fp16) and 2^-38 max |x| sum |w| (x over a power of two that
+                       takes its row's maximum to 2^14 or more: an fp16 subnormal is off by 2^-25); both
+                       + fp32 sums, whose chain is K / 16 adds in the tensor core and at most 64 outside,
+                       2^-22 each;
   activations          |act'| <= 1.13 for every activation here (GELU's maximum is 1.129), and the
                        fast exponential and division are below 2^-18 |p| absolute;
-  backward product     dp rounded to bf16 and the weight rounded to bf16: 2 * 2^-8 + 2^-16 relative,
-                       plus the error of act' (below 2^-18 (1 + |p|) of dy) on each term.
-Such worst cases add up all signs alike, so the whole output is also held to a relative 2-norm of
-2^-8: k independent roundings, each uniform with a root mean square of at most 2^-8 / sqrt 3, give
-sqrt(k / 3) 2^-8, and every output here goes through at most 3.
+  backward product     dp and the weight rounded to fp16, as above: 2 * 2^-11 + 2^-16 relative, 2^-37 of
+                       the row's maximum, plus the error of act' (below 2^-18 (1 + |p|) of dy) on each term.
+Such worst cases add up all signs alike, so the whole output is also held to a relative 2-norm: the
+output's own rounding to bf16 is uniform with a root mean square of at most 2^-8 / sqrt 3; a second one of
+that size (linear's weights) makes it sqrt(2 / 3) 2^-8 < 2^-8, two to fp16 beside it less than 0.6 * 2^-8.
 """
 from __future__ import annotations
 
@@ -22,6 +25,8 @@ from parity import GEMV_XS_COEF
 ACTS = ("none", "relu", "silu", "gelu", "gelu_tanh")
 LIPSCHITZ = 1.13
 STEP = 2.0 ** -8
+HALF_STEP = 2.0 ** -11
+ONE_ROUNDING = 0.6 * STEP
 FAST = 2.0 ** -18
 TINY = 1e-30
 
@@ -67,7 +72,7 @@ def bf(seed, *shape, spread=1.0):
     return (torch.randn(*shape, generator=g) * spread).to(torch.bfloat16)
 
 
-def projection(x, w, layer, gs):
+def projection(x, w, layer, gs, half=False):
     """(x W^T, its error bound before any output rounding) in fp64; x bf16."""
     x = x.double()
     p, mag = x @ w.t(), x.abs() @ w.abs().t()
@@ -76,7 +81,10 @@ def projection(x, w, layer, gs):
         sc = layer[1].view(torch.float16).double()  # [G][N]
         xs = x.abs().reshape(M, K // gs, gs).sum(-1) @ sc
         return p, GEMV_XS_COEF * xs + (K // 128 + 64) * 2.0 ** -22 * mag
-    return p, (STEP + (K // 16 + 64) * 2.0 ** -22) * mag
+    sums = (K // 16 + 64) * 2.0 ** -22
+    if half:
+        return p, (HALF_STEP + sums) * mag + 2.0 ** -38 * x.abs().amax(1, True) * w.abs().sum(1)
+    return p, (STEP + sums) * mag
 
 
 def linear(x, w, layer, gs, bias=None, residual=None, name="none"):
@@ -93,8 +101,8 @@ def linear(x, w, layer, gs, bias=None, residual=None, name="none"):
 
 def gated(x, wg, wu, gate, up, gs, name):
     """(h, bound of h, (g, bound), (u, bound))."""
-    g, eg = projection(x, wg, gate, gs)
-    u, eu = projection(x, wu, up, gs)
+    g, eg = projection(x, wg, gate, gs, half=True)
+    u, eu = projection(x, wu, up, gs, half=True)
     a, _ = act(g, name)
     ea = LIPSCHITZ * eg + FAST * g.abs()
     h = a * u
@@ -102,11 +110,12 @@ def gated(x, wg, wu, gate, up, gs, name):
     return h, e + STEP * (h.abs() + e), (g, eg + STEP * (g.abs() + eg)), (u, eu + STEP * (u.abs() + eu))
 
 
-def _back(dp, slack, w, depth):
+def _back(dp, largest, slack, w, depth):
+    """dp W and its bound; largest: the rows' largest |dp|, over all the products that share its scale."""
     dx = dp @ w
     mag = dp.abs() @ w.abs()
-    e = (2 * STEP + 2.0 ** -16 + (depth // 16 + 64) * 2.0 ** -22) * mag + slack @ w.abs()
-    return dx, e + STEP * (dx.abs() + e)
+    e = (2 * HALF_STEP + 2.0 ** -16 + (depth // 16 + 64) * 2.0 ** -22) * mag + slack @ w.abs()
+    return dx, e + 2.0 ** -37 * largest * w.abs().sum(0) + STEP * (dx.abs() + e)
 
 
 def linear_backward(dy, pre, w, name):
@@ -116,9 +125,7 @@ def linear_backward(dy, pre, w, name):
     da = act(p, name)[1] if name != "none" else torch.ones_like(dy)
     slack = FAST * dy.abs() * (1 + p.abs()) if name != "none" else torch.zeros_like(dy)
     dp = dy * da
-    dx, e = _back(dp, slack, w, w.shape[0])
-    if name == "none":  # dy is the operand as it stands
-        e = e - STEP * (dp.abs() @ w.abs())
+    dx, e = _back(dp, dy.abs().amax(1, True), slack, w, w.shape[0])
     M = dy.shape[0]
     return dx, e, dp.sum(0), slack.sum(0) + M * 2.0 ** -24 * dp.abs().sum(0)
 
@@ -127,8 +134,10 @@ def gated_backward(dh, g, u, wg, wu, name):
     dh, g, u = dh.double(), g.double(), u.double()
     a, da = act(g, name)
     k = FAST * dh.abs() * (1 + g.abs())
-    d1, e1 = _back(dh * u * da, k * u.abs(), wg, 2 * wg.shape[0])
-    d2, e2 = _back(dh * a, k, wu, 2 * wu.shape[0])
+    dg, du = dh * u * da, dh * a
+    largest = torch.maximum(dg.abs().amax(1, True), du.abs().amax(1, True))
+    d1, e1 = _back(dg, largest, k * u.abs(), wg, 2 * wg.shape[0])
+    d2, e2 = _back(du, largest, k, wu, 2 * wu.shape[0])
     return d1 + d2, e1 + e2 + STEP * (d1 + d2).abs()
 
 

@@ -128,3 +128,43 @@ def test_in_place_and_rows_behind():
     g = dh.clone()
     dx2, _ = w4.awq_rmsnorm_backward(dy, h, w, s=s, dh=g, out=g)
     assert torch.equal(dx.view(torch.int16), dx2.view(torch.int16))
+
+
+# more rows than two per SM, with K where the ring's depth or the threads' share changes
+MANY = [(300, 8), (1000, 16), (320, 248), (700, 2056), (400, 8200), (320, 16392), (310, 28672), (310, 32768)]
+
+
+@pytest.mark.parametrize("M,K", MANY)
+def test_many_rows(M, K):
+    x, r, w, s = inputs(M, K, seed=30)
+    y, h = w4.awq_rmsnorm(x.cuda(), w.cuda(), residual=r.cuda(), s=s.cuda(), eps=1e-5)
+    hw, v = ref.norm(x, r, w, s, 1e-5)
+    assert torch.equal(h.double().cpu(), hw)
+    ref.check(y, v, (ref.STEP + 2 * F32) * v.abs(), "y")
+    q, sc, h = w4.awq_rmsnorm_e4m3(x.cuda(), w.cuda(), residual=r.cuda(), s=s.cuda(), eps=1e-5)
+    assert torch.equal(h.double().cpu(), hw)
+    scale = v.abs().amax(1, True) / 448
+    ref.check(sc, scale, 2 * F32 * scale, "scales", norm2=2 * F32)
+    t = v / scale
+    ref.check(q.float(), t, torch.clamp(2.0 ** -4 * t.abs(), min=2.0 ** -10) + 8 * F32 * t.abs(), "q", norm2=2.0 ** -4)
+    d = ref.bf(9, M, K)
+    dx, dw = w4.awq_rmsnorm_backward(x.cuda(), r.cuda(), w.cuda(), s=s.cuda(), dh=d.cuda(), eps=1e-5)
+    want, dww, rstd, v = ref.norm_backward(x, r, w, s, d, 1e-5)
+    xh = r.double() * rstd
+    mag = rstd * (v.abs() + xh.abs() * (v * xh).abs().mean(1, keepdim=True))
+    ref.check(dx, want, ref.STEP * want.abs() + 4 * F32 * mag, "dx")
+    terms = (x.double() * xh / s.double()).abs().sum(0)
+    ref.check(dw, dww, (F32 + M * 2.0 ** -24) * terms, "dweight", norm2=2.0 ** -16 + F32 * 64)
+    w4.check_device_status()
+
+
+def test_non_finite_rows_in_the_backward_pass():
+    """A NaN in a row's gradient spoils that row and, through the sum over rows, dweight; no other row."""
+    h, dy, w, _ = inputs(400, 1024, seed=3)
+    dx0, _ = w4.awq_rmsnorm_backward(dy.cuda(), h.cuda(), w.cuda())
+    dy[5, 3] = float("nan")
+    h[7, 9] = float("inf")
+    dx, dw = w4.awq_rmsnorm_backward(dy.cuda(), h.cuda(), w.cuda())
+    assert torch.isnan(dx[5]).all() and torch.isnan(dw[3])
+    keep = [m for m in range(400) if m not in (5, 7)]
+    assert torch.equal(dx[keep].view(torch.int16), dx0[keep].view(torch.int16))

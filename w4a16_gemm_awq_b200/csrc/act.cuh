@@ -47,30 +47,10 @@ __device__ __forceinline__ float act_grad(float p) {
     }
     if constexpr (ACT == W4A16_ACT_GELU_TANH) {
         const float sg = sigmoid_fast(1.5957691216057308f * fmaf(0.044715f * p * p, p, p));
-        return fmaf(p * sg, (1.0f - sg) * 1.5957691216057308f * fmaf(0.134145f * p, p, 1.0f), sg);
+        const float q = fminf(fabsf(p), 32.0f);  // beyond, sg is 0 or 1, and q^2 must not become infinite beside it
+        return fmaf(p * sg, (1.0f - sg) * 1.5957691216057308f * fmaf(0.134145f * q, q, 1.0f), sg);
     }
     return 1.0f;
-}
-
-// The activation as a run-time value, where it costs nothing against the rest of the kernel.
-__device__ __forceinline__ float act_value(int act, float p) {
-    switch (act) {
-        case W4A16_ACT_RELU: return act_value<W4A16_ACT_RELU>(p);
-        case W4A16_ACT_SILU: return act_value<W4A16_ACT_SILU>(p);
-        case W4A16_ACT_GELU: return act_value<W4A16_ACT_GELU>(p);
-        case W4A16_ACT_GELU_TANH: return act_value<W4A16_ACT_GELU_TANH>(p);
-        default: return p;
-    }
-}
-
-__device__ __forceinline__ float act_grad(int act, float p) {
-    switch (act) {
-        case W4A16_ACT_RELU: return act_grad<W4A16_ACT_RELU>(p);
-        case W4A16_ACT_SILU: return act_grad<W4A16_ACT_SILU>(p);
-        case W4A16_ACT_GELU: return act_grad<W4A16_ACT_GELU>(p);
-        case W4A16_ACT_GELU_TANH: return act_grad<W4A16_ACT_GELU_TANH>(p);
-        default: return 1.0f;
-    }
 }
 
 // The activation of C values held in registers, the choice made once for all of them: a choice per
