@@ -434,7 +434,9 @@ w4a16_status awq_fold_activations(const uint16_t* x, const float* s, uint16_t* x
  * Feed-forward operators around the W4A16 product.  A transformer layer's feed-forward half is
  *     h = x + r;  y = rmsnorm(h) / s;  a = act(y . Wg^T) * (y . Wu^T);  out = a . Wd^T + h
  * and the entry points below are its three steps, with their backward passes through frozen
- * weights (the 4-bit codes have no gradient).  [AWQ translation, 3.2: 1 / s is folded into the
+ * weights (the 4-bit codes have no gradient).  Unless said otherwise, an output overlaps no input.
+ * A call may fetch qweight, scales and zeros while the previous kernel on its stream still runs, if
+ * that is one of these operators': they must not be an output of such a call.  [AWQ translation, 3.2: 1 / s is folded into the
  * preceding operator, which here is the norm.]
  *
  * Activations act(p), and act'(p) in the backward passes, in fp32:
@@ -481,8 +483,9 @@ size_t w4a16_fused_workspace_bytes(int op, int64_t M, int64_t N, int64_t K);
  *             (the addition in place), otherwise y overlaps no input.
  *   pre       [M][N] bf16 bits, output, or NULL: bf16_rne(p), for the backward pass.
  *   activation: w4a16_activation.  group_size: as w4a16_linear_ex.
- *   workspace: required, W4A16_OP_LINEAR.  M >= 1; M <= 16 runs the decode kernel, larger M
- *   the tensor-core kernel, in which each weight is rounded once to bf16.  There is no CSR term.
+ *   workspace: required, W4A16_OP_LINEAR.  M >= 1; M <= 16 runs the decode kernel (exact
+ *   weights), larger M the tensor-core kernel, in which each weight is rounded once to bf16.
+ *   There is no CSR term.
  *   Errors: NULL, SHAPE, ALIGN, VALUE (unknown activation), UNSUPPORTED when called.
  */
 w4a16_status w4a16_linear_fused(const uint16_t* x, const w4a16_weights* weights, const uint16_t* bias,
@@ -496,7 +499,9 @@ w4a16_status w4a16_linear_fused(const uint16_t* x, const w4a16_weights* weights,
  *   dy        [M][N] bf16 bits (also the residual's gradient).
  *   pre       [M][N] bf16 bits, as the forward call wrote it.  Ignored, may be NULL, for NONE.
  *   dx        [M][K] bf16 bits, output.  dbias [N] fp32, output, or NULL.
- *   dp enters the product rounded to bf16 and the sum of dbias in fp32, unrounded.
+ *   dp enters the product in fp16 over a power of two per token, its largest value at 2^13 or
+ *   more, and each weight rounded once to fp16: |(q - z) scale| <= 65504, or it is infinite.
+ *   dbias sums the unrounded fp32 dp.
  *   workspace: required, W4A16_OP_LINEAR_BACKWARD.  Repeated calls give the same bits.
  *   Errors: as w4a16_linear_fused.
  */
@@ -511,6 +516,9 @@ w4a16_status w4a16_linear_fused_backward(const uint16_t* dy, const uint16_t* pre
  *   x [M][K], h [M][F] bf16 bits; gate and up: two layers [F][K] of the same group_size.
  *   g_out, u_out  [M][F] bf16 bits, outputs, or both NULL: bf16_rne(g), bf16_rne(u), for the
  *                 backward pass.
+ *   For M > 16 the operands are fp16 as in w4a16_linear_fused_backward: x over a power of two
+ *   per token, which keeps every bf16 value above 2^-28 of the token's largest as it is, and
+ *   weights rounded once, |(q - z) scale| <= 65504.
  *   workspace: required, W4A16_OP_GATED with N = F.  Otherwise as w4a16_linear_fused (NULL also
  *   when only one of g_out and u_out is given).
  */
@@ -521,8 +529,9 @@ w4a16_status w4a16_gated(const uint16_t* x, const w4a16_weights* gate, const w4a
 /*
  * w4a16_gated_backward -- the gradient of w4a16_gated with respect to x:
  *     dg = dh * u * act'(g);  du = dh * act(g);   dx = bf16_rne( dg . dequant(Qg) + du . dequant(Qu) )
- *   dh, g, u [M][F] bf16 bits; dx [M][K] bf16 bits, output.  dg and du enter the product rounded
- *   to bf16.  workspace: required, W4A16_OP_GATED_BACKWARD with N = F.  Errors: as w4a16_gated.
+ *   dh, g, u [M][F] bf16 bits; dx [M][K] bf16 bits, output.  dg and du enter the product as dp
+ *   does in w4a16_linear_fused_backward, with one power of two per token for both.
+ *   workspace: required, W4A16_OP_GATED_BACKWARD with N = F.  Errors: as w4a16_gated.
  */
 w4a16_status w4a16_gated_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u,
                                   const w4a16_weights* gate, const w4a16_weights* up, uint16_t* dx, int64_t M,

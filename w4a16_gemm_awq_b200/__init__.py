@@ -723,7 +723,7 @@ def _sum_output(x, residual, sum_out, M, K, dev):
 def awq_rmsnorm(x, weight, residual=None, s=None, eps=1e-6, out=None, sum_out=None):
     """(y, h): h = bf16(x + residual), written to sum_out (a new tensor by default; x or residual for
     the addition in place), and y = bf16(h * rsqrt(mean h^2 + eps) * weight / s).  Without a
-    residual h is x itself, unless sum_out is given."""
+    residual h is x itself (overwritten, if out is x), unless sum_out is given."""
     M, K, dev = _norm_operands(x, "x", weight, s)
     if _elsewhere(dev):
         with torch.cuda.device(dev):

@@ -444,10 +444,10 @@ w4a16_status encode_rows(EncodeTiledFn enc, CUtensorMap* map, const uint16_t* p,
 }
 
 // Tensor map of qweight [N][K/8] in boxes of 16 words (128 codes) x 64 rows.
-w4a16_status encode_packed(EncodeTiledFn enc, CUtensorMap* map, const uint32_t* p, int64_t N, int64_t K) {
+w4a16_status encode_packed(EncodeTiledFn enc, CUtensorMap* map, const uint32_t* p, int64_t N, int64_t K, int rows) {
     const cuuint64_t dims[2] = {(cuuint64_t)(K / 8), (cuuint64_t)N};
     const cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
-    const cuuint32_t box[2] = {16, 64};
+    const cuuint32_t box[2] = {16, (cuuint32_t)rows};
     const cuuint32_t estr[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint32_t*>(p), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -508,9 +508,10 @@ w4a16_status run_ffn(int op, const FfnArgs& args, const DeviceInfo& d, void* wor
     FfnMaps maps;
     const CUtensorMapDataType type = op == W4A16_OP_LINEAR ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     st = encode_rows(enc, &maps.x, a.a, a.M, !back ? a.K : two ? 2 * (int64_t)a.N : a.N, plan.bn / 2, type);
-    if (st == W4A16_OK) st = encode_packed(enc, &maps.w, a.w.qweight, a.N, a.K);
+    const int box = op == W4A16_OP_GATED ? 64 : 128;
+    if (st == W4A16_OK) st = encode_packed(enc, &maps.w, a.w.qweight, a.N, a.K, box);
     maps.w2 = maps.w;
-    if (st == W4A16_OK && two) st = encode_packed(enc, &maps.w2, a.w2.qweight, a.N, a.K);
+    if (st == W4A16_OK && two) st = encode_packed(enc, &maps.w2, a.w2.qweight, a.N, a.K, box);
     if (st != W4A16_OK) return st;
     return from_cuda(launch_ffn_gemm(maps, plan, a, back, two, reinterpret_cast<float*>(ws),
                                      static_cast<unsigned*>(workspace), d.status, stream));

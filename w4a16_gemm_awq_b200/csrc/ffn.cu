@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(256) half_rows_kernel(const uint16_t* x, uint1
                                                         int K, int top) {
     __shared__ uint32_t buf[32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the inputs, and the outputs' last readers, belong to the stream order
     constexpr int V = 4;  // chunks of a row that stay in registers
     for (long long m = blockIdx.x; m < M; m += gridDim.x) {
         const uint16_t* row = x + m * K;
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(512) gated_dp_kernel(const uint16_t* dh, const
     __shared__ __align__(8) uint64_t full[kDpDepth];
     extern __shared__ __align__(128) uint16_t ring[];  // KEEP: [depth][dh row, g row, u row]
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the inputs, and the outputs' last readers, belong to the stream order
     const int T = blockDim.x;
     auto load_row = [&](int slot, long long m) {  // thread 0; the slot's earlier row has been read
         mbar_arrive_expect_tx(&full[slot], (uint32_t)(6 * F));
@@ -306,11 +308,13 @@ namespace {
 
 int row_blocks(int64_t M, int num_sms) { return (int)(M < (int64_t)num_sms * 16 ? M : (int64_t)num_sms * 16); }
 
+// A launch whose setup overlaps the previous kernel on the stream; the kernel waits for that one's end.
 template <typename... Args>
-cudaError_t launch_after(void (*fn)(Args...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
+cudaError_t launch_after(void (*fn)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -324,16 +328,16 @@ cudaError_t launch_after(void (*fn)(Args...), dim3 grid, int threads, cudaStream
 
 cudaError_t launch_half_rows(const uint16_t* x, uint16_t* out, float* row_scale, int64_t M, int K, int num_sms,
                              cudaStream_t stream) {
-    half_rows_kernel<<<row_blocks(M, num_sms), 256, 0, stream>>>(x, out, row_scale, M, K, 14);
-    return cudaGetLastError();
+    return launch_after(half_rows_kernel, dim3(row_blocks(M, num_sms)), 256, 0, stream, x, out, row_scale, (long long)M,
+                        K, 14);
 }
 
 cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* row_scale, float* dbias,
                              float* sums, unsigned* counters, int64_t M, int N, int act, int num_sms,
                              cudaStream_t stream) {
     if (act == W4A16_ACT_NONE && dbias == nullptr) return launch_half_rows(dy, dp, row_scale, M, N, num_sms, stream);
-    half_rows_kernel<<<row_blocks(M, num_sms), 256, 0, stream>>>(dy, nullptr, row_scale, M, N, 13);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(half_rows_kernel, dim3(row_blocks(M, num_sms)), 256, 0, stream, dy, (uint16_t*)nullptr,
+                                       row_scale, (long long)M, N, 13);
     if (e != cudaSuccess) return e;
     const int runs = linear_dp_runs(M, N, num_sms);
     const int rows = (int)((M + runs - 1) / runs);
@@ -344,7 +348,7 @@ cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* 
                : act == W4A16_ACT_SILU ? linear_dp_kernel<W4A16_ACT_SILU>
                : act == W4A16_ACT_GELU ? linear_dp_kernel<W4A16_ACT_GELU>
                                        : linear_dp_kernel<W4A16_ACT_GELU_TANH>;
-    return launch_after(fn, grid, 32 * kDpRowThreads, stream, dy, pre, dp, (const float*)row_scale, s, dbias, counters,
+    return launch_after(fn, grid, 32 * kDpRowThreads, 0, stream, dy, pre, dp, (const float*)row_scale, s, dbias, counters,
                         (long long)M, N, rows);
 }
 
@@ -380,8 +384,7 @@ cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_
         const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    fn<<<grid, threads, smem, stream>>>(dh, g, u, dp, row_scale, M, F, depth, err);
-    return cudaGetLastError();
+    return launch_after(fn, dim3(grid), threads, smem, stream, dh, g, u, dp, row_scale, (long long)M, F, depth, err);
 }
 
 }  // namespace w4a16

@@ -19,8 +19,8 @@
 //     per product of a single-CTA tile of the same width.
 //   - The two accumulators (BN fp32 columns each, at TMEM columns 0 and 256) are used in turn, so the
 //     epilogue of one tile runs while the next one accumulates.
-//   - Warp roles (768 threads): 0 TMA of the activations, 1 MMA issue (leader CTA), 2 TMA of the
-//     packed weights, 3 TMEM allocation, 4-11 epilogue (a TMEM lane quarter and half of the columns
+//   - Warp roles (768 threads): 0 TMA of the activations, 1 MMA issue (leader CTA), 2 TMA of the packed
+//     weights, 3 their scales and zero points (and the TMEM), 4-11 epilogue (a TMEM lane quarter and half of the columns
 //     each), 12-23 dequant: three groups of four warps, which take the stages of 64 contraction steps
 //     in turn.
 //   - Dequant.  A ring entry holds the packed weights of 128 x 128 codes (8 KB, 64-byte rows, 64-byte
@@ -56,26 +56,33 @@ constexpr int kGroups = 3;               // dequant groups of four warps
 constexpr int kEpilogue0 = 4, kDequant0 = 12;
 constexpr int kThreads = 32 * (kDequant0 + 4 * kGroups);
 constexpr int kS = 6;                    // stages of 64 contraction steps
-constexpr int kP = 3;                    // packed entries of 128 contraction steps
-// A wait by parity takes a phase for the one two before it.  So a dequant group that uses a slot uses it in
-// every phase: having waited for each phase in turn it can never pass on an old one, in whatever order the
-// copies land.
-static_assert(kS % kGroups == 0 && 2 * kP % kGroups == 0, "the groups meet their slots in every phase");
-constexpr int kABytes = 128 * 128;       // 128 channels x 64 steps, bf16
-constexpr int kBBytes = 128 * 128;       // up to 128 tokens (this CTA's half) x 64 steps, bf16
-constexpr int kEntryBytes = 128 * 64;    // 128 packed rows of 16 words
+constexpr int kABytes = 128 * 128;       // 128 channels x 64 steps, 16 bits each
+constexpr int kEntryBytes = 128 * 64;    // 128 packed rows of 16 words: 128 contraction steps
 constexpr int kParBytes = 512;           // their 128 scales (256 bytes) and 16 words of zero points
-constexpr int kAOff = 0;
-constexpr int kBOff = kAOff + kS * kABytes;
-constexpr int kPOff = kBOff + kS * kBBytes;
-constexpr int kParOff = kPOff + kP * kEntryBytes;
 constexpr int kOutCols = 8;              // columns (tokens) an epilogue warp finishes at a time
 constexpr int kOutStride = 36;           // floats per token in its transposing buffer: 32 channels, padded
-constexpr int kOutOff = kParOff + kP * kParBytes;
 constexpr int kOutBytes = kOutCols * kOutStride * 4;
-constexpr int kBarOff = kOutOff + 8 * kOutBytes;
-constexpr int kSmemBytes = kBarOff + 256;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+
+// Shared memory.  NARROW: tiles of up to 128 tokens, half of the memory per stage of the activations, which
+// goes to the ring of packed weights: with few tokens a stage is short and the weights come from device
+// memory, so more of them have to be on their way.
+template <bool NARROW>
+struct Smem {
+    static constexpr int kP = NARROW ? 6 : 3;               // packed entries
+    static constexpr int kBBytes = (NARROW ? 64 : 128) * 128;  // this CTA's half of the tokens x 64 steps, 16 bits each
+    static constexpr int kAOff = 0;
+    static constexpr int kBOff = kAOff + kS * kABytes;
+    static constexpr int kPOff = kBOff + kS * kBBytes;
+    static constexpr int kParOff = kPOff + kP * kEntryBytes;
+    static constexpr int kOutOff = kParOff + kP * kParBytes;
+    static constexpr int kBarOff = kOutOff + 8 * kOutBytes;
+    static constexpr int kBytes = kBarOff + 256;
+    static_assert(kBytes <= 227 * 1024 && 8 * (2 * kS + 2 * kP + 5) + 8 <= 256, "shared memory of one CTA");
+    // A wait by parity takes a phase for the one two before it.  So a dequant group that uses a slot uses it
+    // in every phase: having waited for each phase in turn it can never pass on an old one, in whatever
+    // order the copies land.
+    static_assert(kP % kGroups == 0 && kS == 2 * kGroups, "the groups meet their slots in every phase");
+};
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemSecond = 256;    // columns of the second accumulator
 
@@ -302,17 +309,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // Barrier among the epilogue warps.
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-template <int MODE>
+template <int MODE, bool NARROW>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                 const __grid_constant__ CUtensorMap map_w2, const GemmArgs2 p) {
+    using S = Smem<NARROW>;
+    constexpr int kP = S::kP;
     // Pointers derive from the array itself, so that the compiler keeps the shared address space.
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {  // the swizzled stages need 1024-byte alignment
         if (threadIdx.x == 0) record_error(p.err, kErrShape);
         return;
     }
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);  // leader: activations landed, weights written
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBarOff);  // leader: activations landed, weights written
     uint64_t* empty = full + kS;     // the MMAs have read the stage
     uint64_t* pfull = empty + kS;    // a packed entry has landed
     uint64_t* pempty = pfull + kP;   // the dequant warps have read it
@@ -334,8 +343,8 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < kP; ++i) {
-            mbar_init(&pfull[i], 1);
-            mbar_init(&pempty[i], 8);
+            mbar_init(&pfull[i], 2);  // rows and parameters
+            mbar_init(&pempty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&dfull[i], 1);
@@ -361,52 +370,66 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     auto fail = [&]() { record_error(p.err, kErrTimeout); };
     Walk w = walk_start(p, pair);
 
-    // One packed entry: 64 packed rows from n with their scales and zero points to each half of the slot.
-    auto load_entry = [&](unsigned slot, int tile, int e) {
-        const int tc = tile % p.tiles_c;
-        uint8_t* dst = smem + kPOff + slot * kEntryBytes;
-        uint8_t* par = smem + kParOff + slot * kParBytes;
-        auto load = [&](int hh, const CUtensorMap* map, const PackedWeights& q, int word, int n, int g) {
-            tma_load_2d(dst + hh * (kEntryBytes / 2), map, &pfull[slot], word, n);
-            bulk_load(par + 128 * hh, q.scales + (size_t)g * p.N + n, 128, &pfull[slot]);
-            bulk_load(par + 256 + 32 * hh, q.zeros + (size_t)g * (p.N >> 3) + (n >> 3), 32, &pfull[slot]);
-        };
-        if (MODE == kLinear) {
-            // the last pair's second half may be past N: its rows go nowhere
-            const int n = tc * 256 + rank * 128;
-            const bool in = n < p.N;
-            mbar_arrive_expect_tx(&pfull[slot], in ? kEntryBytes + 320 : 16);
-            if (in) {
-                load(0, &map_w, p.w, e * 16, n, e / p.gr);
-                load(1, &map_w, p.w, e * 16, n + 64, e / p.gr);
-            } else {
-                bulk_load(par, p.w.scales, 16, &pfull[slot]);
-            }
-        } else if (MODE == kGated) {
-            const int n = tc * 128 + rank * 64;
-            mbar_arrive_expect_tx(&pfull[slot], kEntryBytes + 320);
-            load(0, &map_w, p.w, e * 16, n, e / p.gr);
-            load(1, &map_w2, p.w2, e * 16, n, e / p.gr);
-        } else {
-            const int kt = tc * 2 + rank;
-            mbar_arrive_expect_tx(&pfull[slot], kEntryBytes + 320);
-            if (e < p.entries1) {
-                load(0, &map_w, p.w, kt * 16, e * 128, kt / p.gr);
-                load(1, &map_w, p.w, kt * 16, e * 128 + 64, kt / p.gr);
-            } else {
-                load(0, &map_w2, p.w2, kt * 16, (e - p.entries1) * 128, kt / p.gr);
-                load(1, &map_w2, p.w2, kt * 16, (e - p.entries1) * 128 + 64, kt / p.gr);
-            }
+    // One packed entry: warp 2 loads its 128 packed rows, warp 3 their scales and zero points.  Each issue
+    // costs the warp some 50 cycles, so one warp that did both held few-token calls back (64 tokens,
+    // 8192 x 28672: 53.5 us).
+    auto load_rows = [&](unsigned slot, int tc, int e) {
+        uint8_t* dst = smem + S::kPOff + slot * kEntryBytes;
+        const int n = tc * 256 + rank * 128;
+        if (MODE == kLinear && n >= p.N) {  // the last pair's second half is past N: its rows go nowhere
+            mbar_arrive(&pfull[slot]);
+            return;
         }
+        mbar_arrive_expect_tx(&pfull[slot], kEntryBytes);
+        if (MODE == kLinear) {
+            tma_load_2d(dst, &map_w, &pfull[slot], e * 16, n);
+        } else if (MODE == kGated) {
+            tma_load_2d(dst, &map_w, &pfull[slot], e * 16, n >> 1);
+            tma_load_2d(dst + kEntryBytes / 2, &map_w2, &pfull[slot], e * 16, n >> 1);
+        } else {
+            const bool first = e < p.entries1;
+            tma_load_2d(dst, first ? &map_w : &map_w2, &pfull[slot], n >> 3, (first ? e : e - p.entries1) * 128);
+        }
+    };
+    auto load_params = [&](unsigned slot, int tc, int e) {
+        uint8_t* par = smem + S::kParOff + slot * kParBytes;
+        auto load = [&](const PackedWeights& q, int g, int n, int count, int at) {
+            bulk_load(par + 2 * at, q.scales + (size_t)g * p.N + n, 2 * count, &pfull[slot]);
+            bulk_load(par + 256 + at / 2, q.zeros + (size_t)g * (p.N >> 3) + (n >> 3), count / 2, &pfull[slot]);
+        };
+        const int n = tc * 256 + rank * 128;
+        if (MODE == kLinear && n >= p.N) {
+            mbar_arrive(&pfull[slot]);
+            return;
+        }
+        mbar_arrive_expect_tx(&pfull[slot], 320);
+        if (MODE == kLinear) {
+            load(p.w, e / p.gr, n, 128, 0);
+        } else if (MODE == kGated) {
+            load(p.w, e / p.gr, n >> 1, 64, 0);
+            load(p.w2, e / p.gr, n >> 1, 64, 64);
+        } else {
+            const bool first = e < p.entries1;
+            load(first ? p.w : p.w2, (n >> 7) / p.gr, (first ? e : e - p.entries1) * 128, 128, 0);
+        }
+    };
+    auto load_entry = [&](unsigned slot, int tc, int e) {
+        if (elect_one()) {
+            if (warp == 2)
+                load_rows(slot, tc, e);
+            else
+                load_params(slot, tc, e);
+        }
+        __syncwarp();
     };
     // The first packed entries are what a call waits for first, and they need only this CTA's barriers.
     // (No kernel before this one on the stream writes the weights.)
-    if (warp == 2) {
+    if (warp == 2 || warp == 3) {
         Walk first = w;
-        if (walk_step(first, p, pair, pairs) && elect_one()) {
-            for (int i = 0; i < kP && first.e0 + i < first.e1; ++i) load_entry(i, first.tile, first.e0 + i);
+        if (walk_step(first, p, pair, pairs)) {
+            const int tc = first.tile % p.tiles_c;
+            for (int i = 0; i < kP && first.e0 + i < first.e1; ++i) load_entry(i, tc, first.e0 + i);
         }
-        __syncwarp();
     }
     cluster_sync_all();  // the other CTA's barriers are initialised too
     tc_fence_after();
@@ -430,7 +453,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 }
                 if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)p.bn * 128u);
-                    tma_load_2d_pair(smem + kBOff + slot * kBBytes, &map_x, cluster_map(&full[slot], 0), c * 64, m0);
+                    tma_load_2d_pair(smem + S::kBOff + slot * S::kBBytes, &map_x, cluster_map(&full[slot], 0), c * 64, m0);
                 }
                 __syncwarp();
             }
@@ -438,11 +461,12 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         // every MMA has read its stage and said so in both CTAs before either may leave
         for (unsigned i = s > kS ? s - kS : 0; ok && i < s; ++i) ok = warp_wait(&empty[i % kS], (i / kS) & 1);
         if (!ok && lane == 0) fail();
-    } else if (warp == 2) {
+    } else if (warp == 2 || warp == 3) {
         // ---------------------------------------------------------------- packed weights
         bool ok = true;
         unsigned i = 0;
         for (bool begun = false; ok && walk_step(w, p, pair, pairs); begun = true) {
+            const int tc = w.tile % p.tiles_c;
             for (int e = w.e0; e < w.e1; ++e, ++i) {
                 if (!begun && i < kP) continue;  // loaded above
                 const unsigned slot = i % kP;
@@ -450,8 +474,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                     ok = false;
                     break;
                 }
-                if (elect_one()) load_entry(slot, w.tile, e);
-                __syncwarp();
+                load_entry(slot, tc, e);
             }
         }
         if (!ok && lane == 0) fail();
@@ -462,8 +485,8 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             const uint32_t idesc = (1u << 4) | (MODE == kLinear ? 1u << 7 | 1u << 10 : 0u) | (MODE == kBackward ? 1u << 15 : 0u) |
                                    ((uint32_t)(p.bn >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
             const uint32_t base = smem_u32(smem);
-            const uint64_t a0 = MODE == kBackward ? smem_desc(base + kAOff, 8192, 1024) : smem_desc(base + kAOff, 16, 1024);
-            const uint64_t b0 = smem_desc(base + kBOff, 16, 1024);
+            const uint64_t a0 = MODE == kBackward ? smem_desc(base + S::kAOff, 8192, 1024) : smem_desc(base + S::kAOff, 16, 1024);
+            const uint64_t b0 = smem_desc(base + S::kBOff, 16, 1024);
             constexpr uint32_t kAStep = (MODE == kBackward ? 2048 : 32) >> 4, kBStep = 32 >> 4;  // 16 steps, as descriptors count
             bool ok = true;
             uint32_t slot = 0, phase = 0;
@@ -483,7 +506,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                     }
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint64_t a = a0 + slot * (kABytes >> 4), b = b0 + slot * (kBBytes >> 4);
+                        const uint64_t a = a0 + slot * (kABytes >> 4), b = b0 + slot * (S::kBBytes >> 4);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma_pair(d, a + kk * kAStep, b + kk * kBStep, idesc, (c > 0 || kk > 0) ? 1u : 0u);
@@ -507,12 +530,13 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         }
     } else if (warp >= kDequant0) {
         // ---------------------------------------------------------------- dequant
-        // The groups take the stages in turn.  A thread's packed words of its next stage are read before it
-        // dequantizes the current one, so that the wait for them and the loads stay out of the chain.
+        // The groups take the packed entries, two stages each, in turn.  A thread's packed words of its next
+        // stage are read before it dequantizes the current one, so that the wait for them and the loads stay
+        // out of the chain.
         const int group = (warp - kDequant0) >> 2;
         const int t = threadIdx.x & 127;  // the first dequant warp is the first of four
-        int stages = 0;
-        while (walk_step(w, p, pair, pairs)) stages += 2 * (w.e1 - w.e0);
+        int entries = 0;
+        while (walk_step(w, p, pair, pairs)) entries += w.e1 - w.e0;
         // forward: row t of A (for GATED 16 gate rows, 16 up rows, ...), the half of its 64 bytes that is the
         // stage's; backward: step t % 64 of the stage's half of the packed rows, channels 64 (t / 64) .. + 63
         const int arow = MODE == kBackward ? (t & 63) : t;   // 128-byte row of the A stage
@@ -522,48 +546,60 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             uint4 a, b;
             uint32_t scale, zword;
         };
-        bool ok = true;
-        auto fetch = [&](int s, Packed& q) {
-            const unsigned i = (unsigned)s >> 1, ps = i % kP;
-            const int h = s & 1;
+        auto read = [&](int i, int h, Packed& q) {
+            const unsigned ps = (unsigned)i % kP;
             const int prow = MODE == kLinear ? t
                              : MODE == kGated ? ((t >> 4) & 1) * 64 + 16 * (t >> 5) + (t & 15)
                                               : 64 * h + (t & 63);
             const int half = MODE == kBackward ? t >> 6 : h;
-            if (!warp_wait(&pfull[ps], (i / kP) & 1)) return false;
-            const uint8_t* src = smem + kPOff + ps * kEntryBytes + prow * 64;
+            const uint8_t* src = smem + S::kPOff + ps * kEntryBytes + prow * 64;
             const int x = (prow >> 1) & 3;
             q.a = *reinterpret_cast<const uint4*>(src + (((2 * half) ^ x) << 4));
             q.b = *reinterpret_cast<const uint4*>(src + (((2 * half + 1) ^ x) << 4));
-            const uint8_t* par = smem + kParOff + ps * kParBytes;
+            if (MODE != kBackward && h == 1) return;  // the same row, the same group
+            const uint8_t* par = smem + S::kParOff + ps * kParBytes;
             q.scale = reinterpret_cast<const uint16_t*>(par)[prow];
             q.zword = reinterpret_cast<const uint32_t*>(par + 256)[prow >> 3] >> (4 * (prow & 7));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pempty[ps]);
-            return true;
         };
+        auto landed = [&](int i) { return warp_wait(&pfull[(unsigned)i % kP], ((unsigned)i / kP) & 1); };
+        using Row = typename Dequant<MODE>::Row;
+        bool ok = true;
         Packed cur{}, next{};
-        if (group < stages) ok = fetch(group, cur);
-        for (int s = group; ok && s < stages; s += kGroups) {
-            const typename Dequant<MODE>::Row weights(cur.scale, cur.zword & 15u);
-            if (s + kGroups < stages && !fetch(s + kGroups, next)) {
-                ok = false;
-                break;
-            }
-            const unsigned slot = (unsigned)s % kS;
-            if (s >= kS && !warp_wait(&empty[slot], ((unsigned)s / kS - 1) & 1)) {
-                ok = false;
-                break;
-            }
-            uint8_t* a = smem + kAOff + slot * kABytes + dst;
+        if (group < entries) {
+            ok = landed(group);
+            if (ok) read(group, 0, cur);
+        }
+        for (int i = group; ok && i < entries; i += kGroups) {
+            Row weights(cur.scale, cur.zword & 15u);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4*>(a + ((c << 4) ^ sw)) =
-                    weights(c < 4 ? u4_get(cur.a, c) : u4_get(cur.b, c - 4));
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_pair(cluster_map(&full[slot], 0));
-            cur = next;
+            for (int h = 0; h < 2; ++h) {
+                if (h == 0) {
+                    read(i, 1, next);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pempty[(unsigned)i % kP]);
+                } else {
+                    if (MODE == kBackward) weights = Row(cur.scale, cur.zword & 15u);
+                    if (i + kGroups < entries) {
+                        ok = landed(i + kGroups);
+                        if (!ok) break;
+                        read(i + kGroups, 0, next);
+                    }
+                }
+                const unsigned s = 2 * (unsigned)i + h, slot = s % kS;
+                if (s >= kS && !warp_wait(&empty[slot], (s / kS - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* a = smem + S::kAOff + slot * kABytes + dst;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(a + ((c << 4) ^ sw)) =
+                        weights(c < 4 ? u4_get(cur.a, c) : u4_get(cur.b, c - 4));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(cluster_map(&full[slot], 0));
+                cur = next;
+            }
         }
         if (!ok && lane == 0) fail();
     } else if (warp >= kEpilogue0) {
@@ -572,7 +608,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         const int row = 32 * quarter + lane;  // TMEM lane
         const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
         const int side = (warp - kEpilogue0) >> 2;  // which half of the columns
-        float* const out = reinterpret_cast<float*>(smem + kOutOff + (warp - kEpilogue0) * kOutBytes);
+        float* const out = reinterpret_cast<float*>(smem + S::kOutOff + (warp - kEpilogue0) * kOutBytes);
         griddep_wait();  // the residual, the outputs and the workspace belong to the stream order
         bool ok = true;
         for (unsigned t = 0; walk_step(w, p, pair, pairs); ++t) {
@@ -838,15 +874,19 @@ cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnA
     g.tiles = (int)plan.tiles;
     g.cut = plan.cut;
     g.runs = plan.runs;
-    auto* fn = back ? ffn_gemm_kernel<kBackward> : two ? ffn_gemm_kernel<kGated> : ffn_gemm_kernel<kLinear>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    const bool narrow = plan.bn <= 128;
+    auto* fn = back  ? (narrow ? ffn_gemm_kernel<kBackward, true> : ffn_gemm_kernel<kBackward, false>)
+               : two ? (narrow ? ffn_gemm_kernel<kGated, true> : ffn_gemm_kernel<kGated, false>)
+                     : (narrow ? ffn_gemm_kernel<kLinear, true> : ffn_gemm_kernel<kLinear, false>);
+    const int smem = narrow ? Smem<true>::kBytes : Smem<false>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t busy = plan.tiles > plan.cut ? std::max<int64_t>(plan.tiles - plan.cut, plan.runs) : plan.runs;
     const int pairs = (int)std::min<int64_t>(plan.pairs, busy);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -211,7 +211,8 @@ struct FfnPlan {
 FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms);
 
 // Tensor maps: x: the activations (dp backward), boxes of 64 contraction steps x bn / 2 tokens, 128-byte
-// swizzle; w, w2: qweight [N][K/8], boxes of 16 words x 64 rows, 64-byte swizzle.
+// swizzle; w, w2: qweight [N][K/8], boxes of 16 words x 128 rows (GATED 64), 64-byte
+// swizzle.
 struct FfnMaps {
     CUtensorMap x, w, w2;
 };
