@@ -50,9 +50,10 @@ def test_long_operand_rows(M):
     w4.check_device_status()
 
 
-@pytest.mark.parametrize("M,N", [(1, 128), (17, 384), (2000, 128), (5000, 1152), (513, 8320)])
+@pytest.mark.parametrize("M,N", [(1, 128), (17, 384), (2000, 128), (5000, 1152), (513, 8320), (40, 4224), (200, 16384),
+                                 (40, 16512), (700, 17536)])
 def test_bias_gradient_runs(M, N):
-    """Column sums over one run of rows and over many."""
+    """Column sums over one run of rows and over many, rows within the registers and longer ones."""
     layer, w = ref.pack_layer(N, N, 1024)
     dy, pre = ref.bf(1, M, N), ref.bf(2, M, N, spread=2.0)
     dx, db = w4.w4a16_linear_fused_backward(dy.cuda(), *cuda(layer), pre=pre.cuda(), activation="gelu", bias_grad=True)

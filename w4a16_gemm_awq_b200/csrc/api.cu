@@ -943,9 +943,11 @@ w4a16_status w4a16_linear_fused_backward(const uint16_t* dy, const uint16_t* pre
     const FusedLayout L = fused_layout(W4A16_OP_LINEAR_BACKWARD, M, N, K, d->num_sms);
     float* row_scale = reinterpret_cast<float*>(ws + L.row_scale);
     uint16_t* dp = reinterpret_cast<uint16_t*>(ws + L.operand);
-    st = from_cuda(launch_linear_dp(dy, pre, dp, row_scale, dbias, reinterpret_cast<float*>(ws + L.sums),
-                                    static_cast<unsigned*>(workspace), M, (int)N, activation, d->num_sms, s));
+    float* sums = dbias != nullptr ? reinterpret_cast<float*>(ws + L.sums) : nullptr;
+    st = from_cuda(launch_linear_dp(dy, pre, dp, row_scale, sums, &a.sum_rows, M, (int)N, activation, d->num_sms, d->status, s));
     if (st != W4A16_OK) return st;
+    a.sums = sums;
+    a.dbias = dbias;
     a.a = dp;
     a.row_scale = row_scale;
     a.y = dx;

@@ -7,10 +7,9 @@
 // of at most 2^-39 of it is left, under the fp32 sums' own; gradients are rounded to 11 bits.
 //
 // Memory bound: 16-byte loads and stores, each row read from device memory once (a second pass over a
-// row comes from the caches).  The bias sums are taken in the same pass as the gradients: a block covers
-// 256 columns x a run of rows and leaves its fp32 column sums in the workspace; the last block of a
-// column range to arrive (a counter, reset to zero) adds them in the order of the runs, so no second
-// launch is needed and the bits do not depend on which is last.
+// row comes from the caches).  The bias gradient's column sums are taken in the same pass as the gradients:
+// each block leaves its rows' fp32 sums in the workspace, and the product's epilogue warps add them up while
+// its first tile accumulates.  The order of the additions is fixed.
 #include "act.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -111,16 +110,14 @@ __global__ void __launch_bounds__(256) half_rows_kernel(const uint16_t* x, uint1
     }
 }
 
-// dp = fp16(dy * act'(pre) / row_scale) over `rows` rows per block.  sums: [gridDim.y][N], nullptr without
-// a bias gradient.
+// Rows too long for linear_dp_kernel's registers: dp = fp16(dy * act'(pre) / row_scale), with the scales from
+// half_rows_kernel, over `rows` rows per block.  sums: [gridDim.y][N], nullptr without a bias gradient.
 template <int ACT>
-__global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_kernel(const uint16_t* dy, const uint16_t* pre,
-                                                                       uint16_t* dp, const float* row_scale,
-                                                                       float* sums, float* dbias, unsigned* counters,
-                                                                       long long M, int N, int rows) {
+__global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_long_kernel(const uint16_t* dy, const uint16_t* pre,
+                                                                            uint16_t* dp, const float* row_scale,
+                                                                            float* sums, long long M, int N, int rows) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
     __shared__ float part[kDpRowThreads][kDpCols];
-    __shared__ int last;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' scales come from the kernel before
     const int lane = threadIdx.x & 31, rt = threadIdx.x >> 5;
     const int n = blockIdx.x * kDpCols + lane * 8;
@@ -151,31 +148,106 @@ __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_kernel(const uin
     for (int e = 0; e < 8; ++e) part[rt][lane * 8 + e] = a[e];
     __syncthreads();
     const int c = threadIdx.x & (kDpCols - 1), nc = blockIdx.x * kDpCols + c;  // one column per thread
-    const bool mine = threadIdx.x < kDpCols && nc < N;
+    if (threadIdx.x >= kDpCols || nc >= N) return;
     float s = 0.0f;
 #pragma unroll
     for (int r = 0; r < kDpRowThreads; ++r) s += part[r][c];
-    if (gridDim.y == 1) {
-        if (mine) dbias[nc] = s;
-        return;
-    }
-    if (mine) __stcg(sums + (size_t)blockIdx.y * N + nc, s);
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        last = atomic_add_acq_rel_gpu(counters + blockIdx.x, 1u) == gridDim.y - 1;
-        if (last) atomicExch(counters + blockIdx.x, 0u);
-    }
-    __syncthreads();
-    if (!last || !mine) return;
-    __threadfence();
-    s = 0.0f;
-#pragma unroll 8
-    for (int r = 0; r < (int)gridDim.y; ++r) s += __ldcg(sums + (size_t)r * N + nc);
-    dbias[nc] = s;
+    sums[(size_t)blockIdx.y * N + nc] = s;
 }
 
 constexpr int kDpDepth = 4;
+
+// dp = fp16(dy * act'(pre) / row_scale), one row per block at a time, V chunks of 8 columns per thread.  Rows
+// come through a ring of `depth` as in gated_dp_kernel; a row's values and the block's column sums stay in
+// registers.  sums: [gridDim.x][N], nullptr without a bias gradient.  (1023 x 5120 with GELU: 13 us from
+// device memory; the two kernels for longer rows, of which the first reads dy for the scales, take 17 us
+// and that read.)
+template <int ACT, int V>
+__global__ void __launch_bounds__(512) linear_dp_kernel(const uint16_t* dy, const uint16_t* pre, uint16_t* dp,
+                                                        float* row_scale, float* sums, long long M, int N, int depth,
+                                                        unsigned* err) {
+    constexpr int kSrcs = ACT == W4A16_ACT_NONE ? 1 : 2;
+    __shared__ uint32_t buf[32];
+    __shared__ __align__(8) uint64_t full[kDpDepth];
+    extern __shared__ __align__(128) uint16_t ring[];  // [depth][dy row, pre row]
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the inputs, and the outputs' last readers, belong to the stream order
+    const int T = blockDim.x;
+    auto load_row = [&](int slot, long long m) {  // thread 0; the slot's earlier row has been read
+        mbar_arrive_expect_tx(&full[slot], (uint32_t)(2 * N * kSrcs));
+        uint16_t* dst = ring + (size_t)slot * kSrcs * N;
+        bulk_load(dst, dy + (size_t)m * N, (uint32_t)(2 * N), &full[slot]);
+        if (kSrcs == 2) bulk_load(dst + N, pre + (size_t)m * N, (uint32_t)(2 * N), &full[slot]);
+    };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < depth; ++i) mbar_init(&full[i], 1);
+        fence_mbarrier_init();
+        for (int i = 0; i < depth; ++i) {
+            const long long m = blockIdx.x + (long long)i * gridDim.x;
+            if (m < M) load_row(i, m);
+        }
+    }
+    __syncthreads();
+    float acc[V][8] = {};
+    int slot = 0;
+    uint32_t phase = 0;
+    bool dead = false;
+    for (long long m = blockIdx.x; m < M; m += gridDim.x) {
+        const uint16_t* src = ring + (size_t)slot * kSrcs * N;
+        if (!dead && !mbar_wait_bounded(&full[slot], phase)) {  // as in gated_dp_kernel
+            dead = true;
+            record_error(err, kErrTimeout);
+        }
+        float v[V][8];
+        uint32_t mx = 0u;
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int k = (c * T + threadIdx.x) * 8;
+            if (k < N) {
+                unpack8(*reinterpret_cast<const uint4*>(src + k), v[c]);
+                if constexpr (kSrcs == 2) {
+                    float q[8];
+                    unpack8(*reinterpret_cast<const uint4*>(src + N + k), q);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[c][e] *= act_grad<ACT>(q[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    acc[c][e] += v[c][e];
+                    mx = max(mx, __float_as_uint(v[c][e]) & 0x7FFFFFFFu);
+                }
+            }
+        }
+        const int e = token_exponent(block_max(mx, buf), 14);
+        const long long next = m + (long long)depth * gridDim.x;  // every thread has its part of the row
+        if (threadIdx.x == 0 && next < M) load_row(slot, next);
+        if (++slot == depth) {
+            slot = 0;
+            phase ^= 1;
+        }
+        if (threadIdx.x == 0) row_scale[m] = exp2_int(e);
+        const float s = exp2_int(-e);
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int k = (c * T + threadIdx.x) * 8;
+            if (k < N) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[c][i] *= s;
+                *reinterpret_cast<uint4*>(dp + (size_t)m * N + k) = pack8_half(v[c]);
+            }
+        }
+    }
+    if (sums == nullptr) return;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+        const int k = (c * T + threadIdx.x) * 8;
+        if (k < N) {
+            float4* dst = reinterpret_cast<float4*>(sums + (size_t)blockIdx.x * N + k);
+            dst[0] = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
+            dst[1] = make_float4(acc[c][4], acc[c][5], acc[c][6], acc[c][7]);
+        }
+    }
+}
 
 // dg = dh u act'(g), du = dh act(g), both in fp16 over the row's scale, side by side in dp [M][2 F]; one
 // row per block at a time.  KEEP (F <= 32 threads): rows come by bulk copies through a ring of `depth`,
@@ -295,10 +367,16 @@ __global__ void __launch_bounds__(512) gated_dp_kernel(const uint16_t* dh, const
 
 }  // namespace
 
-// Runs of rows: blocks for one round of two per SM, at least 16 rows each, and few enough that adding the
-// runs up (one load per run and column in the last block) stays short.  (64 runs at 1023 x 5120 took
-// 20 us, most of it in those sums.)
+// Rows of column sums.  Up to 16384 columns one per block; two blocks per SM where two rows each fit beside
+// one another (1023 x 5120 with GELU: 13 us, 14 us with one).  Beyond, runs of rows: blocks for one round of
+// two per SM, at least 16 rows each, and few enough that adding the runs up stays short.
+constexpr int kDpLongest = 16384;  // 512 threads with four chunks each
+
 int linear_dp_runs(int64_t M, int N, int num_sms) {
+    if (N <= kDpLongest) {
+        const int64_t blocks = (int64_t)num_sms * (N <= 8192 ? 2 : 1);
+        return (int)(M < blocks ? M : blocks);
+    }
     const int64_t cols = (N + kDpCols - 1) / kDpCols, most = (M + kDpRowThreads - 1) / kDpRowThreads;
     const int64_t runs = 2 * num_sms / cols;
     return (int)(runs < 1 ? 1 : runs > 32 ? (most < 32 ? most : 32) : runs > most ? most : runs);
@@ -332,24 +410,50 @@ cudaError_t launch_half_rows(const uint16_t* x, uint16_t* out, float* row_scale,
                         K, 14);
 }
 
-cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* row_scale, float* dbias,
-                             float* sums, unsigned* counters, int64_t M, int N, int act, int num_sms,
-                             cudaStream_t stream) {
-    if (act == W4A16_ACT_NONE && dbias == nullptr) return launch_half_rows(dy, dp, row_scale, M, N, num_sms, stream);
+cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* row_scale, float* sums,
+                             int* sum_rows, int64_t M, int N, int act, int num_sms, unsigned* err, cudaStream_t stream) {
+    *sum_rows = 0;
+    if (act == W4A16_ACT_NONE && sums == nullptr) return launch_half_rows(dy, dp, row_scale, M, N, num_sms, stream);
+    const int runs = linear_dp_runs(M, N, num_sms);
+    if (N <= kDpLongest) {
+        const int V = N <= 4096 ? 1 : N <= 8192 ? 2 : 4, threads = (N / (8 * V) + 31) / 32 * 32;
+        const size_t row = (size_t)2 * N * (act == W4A16_ACT_NONE ? 1 : 2);
+        const size_t ring = N <= 8192 ? 100 * 1024 : 200 * 1024;
+        const int depth = row * kDpDepth <= ring ? kDpDepth : (int)(ring / row);
+        const size_t smem = depth * row;
+        using Kernel = void (*)(const uint16_t*, const uint16_t*, uint16_t*, float*, float*, long long, int, int, unsigned*);
+        Kernel fn = nullptr;
+#define W4A16_DP(ACT) \
+    case ACT: fn = V == 1 ? linear_dp_kernel<ACT, 1> : V == 2 ? linear_dp_kernel<ACT, 2> : linear_dp_kernel<ACT, 4>; break
+        switch (act) {
+            W4A16_DP(W4A16_ACT_NONE);
+            W4A16_DP(W4A16_ACT_RELU);
+            W4A16_DP(W4A16_ACT_SILU);
+            W4A16_DP(W4A16_ACT_GELU);
+            W4A16_DP(W4A16_ACT_GELU_TANH);
+            default: return cudaErrorInvalidValue;
+        }
+#undef W4A16_DP
+        if (smem > 32 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+        }
+        if (sums != nullptr) *sum_rows = runs;
+        return launch_after(fn, dim3(runs), threads, smem, stream, dy, pre, dp, row_scale, sums, (long long)M, N, depth, err);
+    }
     const cudaError_t e = launch_after(half_rows_kernel, dim3(row_blocks(M, num_sms)), 256, 0, stream, dy, (uint16_t*)nullptr,
                                        row_scale, (long long)M, N, 13);
     if (e != cudaSuccess) return e;
-    const int runs = linear_dp_runs(M, N, num_sms);
     const int rows = (int)((M + runs - 1) / runs);
     const dim3 grid((N + kDpCols - 1) / kDpCols, (unsigned)((M + rows - 1) / rows));
-    float* s = dbias != nullptr ? sums : nullptr;
-    auto* fn = act == W4A16_ACT_NONE   ? linear_dp_kernel<W4A16_ACT_NONE>
-               : act == W4A16_ACT_RELU ? linear_dp_kernel<W4A16_ACT_RELU>
-               : act == W4A16_ACT_SILU ? linear_dp_kernel<W4A16_ACT_SILU>
-               : act == W4A16_ACT_GELU ? linear_dp_kernel<W4A16_ACT_GELU>
-                                       : linear_dp_kernel<W4A16_ACT_GELU_TANH>;
-    return launch_after(fn, grid, 32 * kDpRowThreads, 0, stream, dy, pre, dp, (const float*)row_scale, s, dbias, counters,
-                        (long long)M, N, rows);
+    if (sums != nullptr) *sum_rows = (int)grid.y;
+    auto* fn = act == W4A16_ACT_NONE   ? linear_dp_long_kernel<W4A16_ACT_NONE>
+               : act == W4A16_ACT_RELU ? linear_dp_long_kernel<W4A16_ACT_RELU>
+               : act == W4A16_ACT_SILU ? linear_dp_long_kernel<W4A16_ACT_SILU>
+               : act == W4A16_ACT_GELU ? linear_dp_long_kernel<W4A16_ACT_GELU>
+                                       : linear_dp_long_kernel<W4A16_ACT_GELU_TANH>;
+    return launch_after(fn, grid, 32 * kDpRowThreads, 0, stream, dy, pre, dp, (const float*)row_scale, sums, (long long)M, N,
+                        rows);
 }
 
 cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dp, float* row_scale,

@@ -98,6 +98,9 @@ struct GemmArgs2 {
     float* partials;
     unsigned* counters;
     unsigned* err;
+    const float* sums;       // BACKWARD: [sum_rows][N] column sums, added up into dbias; or sum_rows = 0
+    float* dbias;
+    int sum_rows;
     const float* row_scale;  // [M] what a token's sums are multiplied by (not for LINEAR)
     int M, N, K;       // N: rows of one weight matrix
     int gr;            // group size / 128
@@ -610,6 +613,23 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         const int side = (warp - kEpilogue0) >> 2;  // which half of the columns
         float* const out = reinterpret_cast<float*>(smem + S::kOutOff + (warp - kEpilogue0) * kOutBytes);
         griddep_wait();  // the residual, the outputs and the workspace belong to the stream order
+        if (MODE == kBackward && p.sum_rows > 0) {
+            // the bias gradient, while the first tile accumulates: 32 columns per CTA, the rows shared by the warps
+            const int first = warp - kEpilogue0;
+            for (int n = (int)blockIdx.x * 32; n < p.N; n += (int)gridDim.x * 32) {
+                float s = 0.0f;
+#pragma unroll 8
+                for (int r = first; r < p.sum_rows; r += 8) s += __ldcg(p.sums + (size_t)r * p.N + n + lane);
+                out[lane] = s;
+                epilogue_barrier();
+                if (first == 0) {
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) s += out[i * (kOutBytes / 4) + lane];
+                    p.dbias[n + lane] = s;
+                }
+                epilogue_barrier();
+            }
+        }
         bool ok = true;
         for (unsigned t = 0; walk_step(w, p, pair, pairs); ++t) {
             const unsigned buf = t & 1;
@@ -862,6 +882,9 @@ cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnA
     g.counters = counters;
     g.err = err;
     g.row_scale = a.row_scale;
+    g.sums = a.sums;
+    g.dbias = a.dbias;
+    g.sum_rows = a.sum_rows;
     g.M = (int)a.M;
     g.N = a.N;
     g.K = a.K;

@@ -194,6 +194,9 @@ struct FfnArgs {
     uint16_t* y;
     uint16_t* pre;
     uint16_t* pre2;
+    const float* sums;  // backward: sum_rows rows of N column sums, added up into dbias; or sum_rows = 0
+    float* dbias;
+    int sum_rows;
     int64_t M;
     int N, K, group_size, act;
 };
@@ -211,8 +214,7 @@ struct FfnPlan {
 FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms);
 
 // Tensor maps: x: the activations (dp backward), boxes of 64 contraction steps x bn / 2 tokens, 128-byte
-// swizzle; w, w2: qweight [N][K/8], boxes of 16 words x 128 rows (GATED 64), 64-byte
-// swizzle.
+// swizzle; w, w2: qweight [N][K/8], boxes of 16 words x 128 rows (GATED 64), 64-byte swizzle.
 struct FfnMaps {
     CUtensorMap x, w, w2;
 };
@@ -224,12 +226,12 @@ cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnA
 cudaError_t launch_half_rows(const uint16_t* x, uint16_t* out, float* row_scale, int64_t M, int K, int num_sms,
                              cudaStream_t stream);
 
-// The gradients before the activation, in the same form (gated: dg and du side by side, [M][2 F]).  sums: linear_dp_runs x N fp32, used with
-// dbias; counters: one per 256 columns, zero between calls.
+// The gradients before the activation, in the same form (gated: dg and du side by side, [M][2 F]).  sums:
+// column sums of dp, linear_dp_runs x N fp32 at most, nullptr without a bias gradient; *sum_rows: how many rows
+// of them the kernel writes.
 int linear_dp_runs(int64_t M, int N, int num_sms);
-cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* row_scale, float* dbias,
-                             float* sums, unsigned* counters, int64_t M, int N, int act, int num_sms,
-                             cudaStream_t stream);
+cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* row_scale, float* sums,
+                             int* sum_rows, int64_t M, int N, int act, int num_sms, unsigned* err, cudaStream_t stream);
 cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dp, float* row_scale,
                             int64_t M, int F, int act, int num_sms, unsigned* err,
                             cudaStream_t stream);
