@@ -454,25 +454,28 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_backward_kernel(const NormBwdArg
     }
 }
 
-// dweight[k] = (sum over the R rows of partials) / s[k]: 32 columns per block, 8 row strides side by
+// dweight[k] = (sum over the R rows of partials) / s[k]: 32 columns per block, kSumRows row strides side by
 // side, joined in a fixed order.
-__global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* partials, const float* s, float* dweight,
-                                                              int R, int K) {
-    __shared__ float part[8][32];
+constexpr int kSumRows = 16;
+
+__global__ void __launch_bounds__(32 * kSumRows) rmsnorm_dweight_kernel(const float* partials, const float* s,
+                                                                        float* dweight, int R, int K) {
+    __shared__ float part[kSumRows][32];
     const int lane = threadIdx.x & 31, rt = threadIdx.x >> 5;
     const int k = blockIdx.x * 32 + lane;
+    const float scale = s != nullptr && rt == 0 && k < K ? s[k] : 1.0f;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are complete
     float a = 0.0f;
     if (k < K) {
-#pragma unroll 8
-        for (int r = rt; r < R; r += 8) a += partials[(size_t)r * K + k];
+#pragma unroll 10
+        for (int r = rt; r < R; r += kSumRows) a += __ldcg(partials + (size_t)r * K + k);
     }
     part[rt][lane] = a;
     __syncthreads();
     if (rt != 0 || k >= K) return;
 #pragma unroll
-    for (int r = 1; r < 8; ++r) a += part[r][lane];
-    dweight[k] = s != nullptr ? a / s[k] : a;
+    for (int r = 1; r < kSumRows; ++r) a += part[r][lane];
+    dweight[k] = s != nullptr ? a / scale : a;
 }
 
 int up32(int v) { return (v + 31) / 32 * 32; }
@@ -596,7 +599,7 @@ cudaError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const
     // the sums' kernel is scheduled while the rows are still walked and waits for their end
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((K + 31) / 32, 1, 1);
-    cfg.blockDim = dim3(256, 1, 1);
+    cfg.blockDim = dim3(32 * kSumRows, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
