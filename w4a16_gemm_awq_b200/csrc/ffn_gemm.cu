@@ -20,11 +20,11 @@
 //   - The two accumulators (BN fp32 columns each, at TMEM columns 0 and 256) are used in turn, so the
 //     epilogue of one tile runs while the next one accumulates.
 //   - Warp roles (768 threads): 0 TMA of the activations, 1 MMA issue (leader CTA), 2 TMA of the packed
-//     weights, 3 their scales and zero points (and the TMEM), 4-11 epilogue (a TMEM lane quarter and half of the columns
-//     each), 12-23 dequant: three groups of four warps, which take the stages of 64 contraction steps
-//     in turn.
+//     weights, 3 their scales and zero points (and the TMEM), 4-11 epilogue (a TMEM lane quarter and half
+//     of the columns each), 12-23 dequant: three groups of four warps, which take the packed entries, two
+//     stages of 64 contraction steps each, in turn.
 //   - Dequant.  A ring entry holds the packed weights of 128 x 128 codes (8 KB, 64-byte rows, 64-byte
-//     swizzle).  A thread turns 8 words into 64 bf16 and stores them as 16-byte chunks of the A stage
+//     swizzle).  A thread turns 8 words into 64 weights and stores them as 16-byte chunks of the A stage
 //     in the layout that the MMA reads, conflict-free.  Forward products contract over k, so a packed
 //     row becomes a row of A (K-major).  The backward product contracts over n, so a packed row
 //     becomes a column of A: it is stored as it lies and the MMA reads A channel-major (MN-major).
@@ -39,6 +39,10 @@
 //     into equal runs, one per pair, whose fp32 partial tiles meet in the workspace: the last to arrive
 //     adds them in the order of the runs, so the bits do not depend on which that is.  The cut tiles
 //     come first, so that joining them hides behind whole tiles.  No pair waits for another.
+//   - Bound: with many tokens the tensor pipe, 96 % busy (4096 tokens, K 4096, F 14336: 598 us alone, 1.61
+//     PFLOP/s; 706 to 742 us in a row of calls, at the clock that the power limit leaves).  With few, the
+//     loads and the dequant, about as long as one another (32 tokens, 16384 x 18944: 61 us, 2.5 TB/s of
+//     packed weights; 56 us with the dequant's arithmetic left out).
 //   - Every wait is bounded; one that runs out records kErrTimeout and its role stops.  All roles of
 //     both CTAs then meet at the closing cluster barrier, since each of their waits is bounded too.
 #include <algorithm>
@@ -65,7 +69,8 @@ constexpr int kOutBytes = kOutCols * kOutStride * 4;
 
 // Shared memory.  NARROW: tiles of up to 128 tokens, half of the memory per stage of the activations, which
 // goes to the ring of packed weights: with few tokens a stage is short and the weights come from device
-// memory, so more of them have to be on their way.
+// memory, so more of them have to be on their way (32 tokens, 16384 x 18944: 70.4 us with three entries, 66.3
+// with six and no less with nine, before the dequant took whole entries).
 template <bool NARROW>
 struct Smem {
     static constexpr int kP = NARROW ? 6 : 3;               // packed entries
@@ -373,9 +378,8 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     auto fail = [&]() { record_error(p.err, kErrTimeout); };
     Walk w = walk_start(p, pair);
 
-    // One packed entry: warp 2 loads its 128 packed rows, warp 3 their scales and zero points.  Each issue
-    // costs the warp some 50 cycles, so one warp that did both held few-token calls back (64 tokens,
-    // 8192 x 28672: 53.5 us).
+    // One packed entry: warp 2 loads its 128 packed rows, warp 3 their scales and zero points (one warp for
+    // both held few-token calls back: backward 32 tokens, 16384 x 18432, 60.6 us instead of 57.0).
     auto load_rows = [&](unsigned slot, int tc, int e) {
         uint8_t* dst = smem + S::kPOff + slot * kEntryBytes;
         const int n = tc * 256 + rank * 128;
