@@ -434,10 +434,10 @@ w4a16_status awq_fold_activations(const uint16_t* x, const float* s, uint16_t* x
  * Feed-forward operators around the W4A16 product.  A transformer layer's feed-forward half is
  *     h = x + r;  y = rmsnorm(h) / s;  a = act(y . Wg^T) * (y . Wu^T);  out = a . Wd^T + h
  * and the entry points below are its three steps, with their backward passes through frozen
- * weights (the 4-bit codes have no gradient).  Unless said otherwise, an output overlaps no input.
- * A call may fetch qweight, scales and zeros while the previous kernel on its stream still runs, if
- * that is one of these operators': they must not be an output of such a call.  [AWQ translation, 3.2: 1 / s is folded into the
- * preceding operator, which here is the norm.]
+ * weights (the 4-bit codes have no gradient).  [AWQ translation, 3.2: 1 / s is folded into the
+ * preceding operator, which here is the norm.]  Unless said otherwise, an output overlaps no input.
+ * Launch overlap: with M <= 16 the forward calls are w4a16_gemv's kernel and follow its rule on
+ * weights; all others read nothing that the previous kernel on the stream may still write.
  *
  * Activations act(p), and act'(p) in the backward passes, in fp32:
  *   NONE p;  RELU max(p, 0), derivative 0 at 0;  SILU p / (1 + e^-p);

@@ -69,12 +69,19 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* buf) {
     return v;
 }
 
+// Waits for the previous kernel on the stream, which the launch overlapped, and lets the next one be scheduled: in
+// this order, so that whatever was complete before this kernel is so for the product, which fetches weights at
+// once.
+__device__ __forceinline__ void stream_order() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // One block per row: row_scale[m] = 2^e, and out = fp16(x 2^-e) unless out is nullptr.
 __global__ void __launch_bounds__(256) half_rows_kernel(const uint16_t* x, uint16_t* out, float* row_scale, long long M,
                                                         int K, int top) {
     __shared__ uint32_t buf[32];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the inputs, and the outputs' last readers, belong to the stream order
+    stream_order();
     constexpr int V = 4;  // chunks of a row that stay in registers
     for (long long m = blockIdx.x; m < M; m += gridDim.x) {
         const uint16_t* row = x + m * K;
@@ -116,9 +123,8 @@ template <int ACT>
 __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_long_kernel(const uint16_t* dy, const uint16_t* pre,
                                                                             uint16_t* dp, const float* row_scale,
                                                                             float* sums, long long M, int N, int rows) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
     __shared__ float part[kDpRowThreads][kDpCols];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' scales come from the kernel before
+    stream_order();  // the rows' scales come from the kernel before
     const int lane = threadIdx.x & 31, rt = threadIdx.x >> 5;
     const int n = blockIdx.x * kDpCols + lane * 8;
     const bool in = n < N;
@@ -170,8 +176,7 @@ __global__ void __launch_bounds__(512) linear_dp_kernel(const uint16_t* dy, cons
     __shared__ uint32_t buf[32];
     __shared__ __align__(8) uint64_t full[kDpDepth];
     extern __shared__ __align__(128) uint16_t ring[];  // [depth][dy row, pre row]
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the inputs, and the outputs' last readers, belong to the stream order
+    stream_order();
     const int T = blockDim.x;
     auto load_row = [&](int slot, long long m) {  // thread 0; the slot's earlier row has been read
         mbar_arrive_expect_tx(&full[slot], (uint32_t)(2 * N * kSrcs));
@@ -262,8 +267,7 @@ __global__ void __launch_bounds__(512) gated_dp_kernel(const uint16_t* dh, const
     __shared__ uint32_t buf[32];
     __shared__ __align__(8) uint64_t full[kDpDepth];
     extern __shared__ __align__(128) uint16_t ring[];  // KEEP: [depth][dh row, g row, u row]
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may set up meanwhile
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the inputs, and the outputs' last readers, belong to the stream order
+    stream_order();
     const int T = blockDim.x;
     auto load_row = [&](int slot, long long m) {  // thread 0; the slot's earlier row has been read
         mbar_arrive_expect_tx(&full[slot], (uint32_t)(6 * F));
