@@ -117,6 +117,7 @@ struct GemmArgs2 {
     int tiles;
     int cut;           // tiles 0 .. cut - 1 are cut into runs
     int runs;          // runs over the cut tiles' entries
+    int halves;        // cut tiles are joined by halves of their columns
 };
 
 // Unit u of `units`, cut into `runs` equal runs: run p starts at p * units / runs.
@@ -649,172 +650,177 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             const int tc = w.tile % p.tiles_c;
             const int m0 = (w.tile / p.tiles_c) * p.bn;
             const int mtile = min(p.bn, p.M - m0);  // tokens of this tile
-            const int mid = ((mtile + 31) >> 5) << 4;  // columns of the first side, a multiple of 16
-            const int cb = side ? min(mid, mtile) : 0, mlim = side ? mtile : min(mid, mtile);  // this warp's
             // partial tiles, token-major: [run + tile][rank][bn][128]
             float* part0 = p.partials + ((size_t)(w.first + w.tile) * 2 + rank) * p.bn * 128 + row;
             const size_t part_step = (size_t)2 * p.bn * 128;
-            if (w.partial) {
-                // A contributor that finds all the others counted joins them with its own accumulator; any
-                // other publishes its partial tile first and then counts itself, and joins if that made it
-                // the last.  The sum goes by the order of the runs either way, so its bits do not depend on
-                // who joins.
-                unsigned* counter = p.counters + 2 * w.tile + rank;
-                const unsigned others = (unsigned)(w.count - 1);
-                if (warp == kEpilogue0 && lane == 0) *last_flag = ld_acquire_gpu(counter) == others;
-                epilogue_barrier();
-                bool last = *reinterpret_cast<volatile int*>(last_flag) != 0;
-                epilogue_barrier();
-                if (!last) {
-                    float* mine = part0 + w.index * part_step;
+            // Where the contributors of a cut tile end together (plan.halves), they take its columns by halves,
+            // the odd ones the second half first: each then finds one half of the others published and joins
+            // it, instead of all publishing all and one joining all.
+            const int mid = min(((mtile + 31) >> 5) << 4, mtile);  // a multiple of 16, or all
+            const bool halves = w.partial && p.halves;
 #pragma unroll 1
-                    for (int c0 = cb; c0 < mlim; c0 += 16) {
-                        uint32_t r[16];
-                        tmem_ld_32x32b_x16(d + (uint32_t)c0, r);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) __stcg(mine + (size_t)(c0 + j) * 128, __uint_as_float(r[j]));
-                    }
-                    __threadfence();
+            for (int part = 0; part < (halves ? 2 : 1); ++part) {
+                const int half = halves ? part ^ (w.index & 1) : 0;
+                const int lo = half ? mid : 0, len = (halves && !half ? mid : mtile) - lo;
+                const int cut = lo + min(((len + 31) >> 5) << 4, len);  // between the sides
+                const int cb = side ? cut : lo, mlim = side ? lo + len : cut;  // this warp's columns
+                if (w.partial) {
+                    // A contributor that finds all the others counted joins them with its own accumulator; any
+                    // other publishes its partial tile first and then counts itself, and joins if that made it
+                    // the last.  The sum goes by the order of the runs either way, so its bits do not depend on
+                    // who joins.
+                    unsigned* counter = p.counters + 4 * w.tile + 2 * rank + half;
+                    const unsigned others = (unsigned)(w.count - 1);
+                    if (warp == kEpilogue0 && lane == 0) *last_flag = ld_acquire_gpu(counter) == others;
                     epilogue_barrier();
-                    if (warp == kEpilogue0 && lane == 0) *last_flag = atomic_add_acq_rel_gpu(counter, 1u) == others;
-                    epilogue_barrier();
-                    last = *reinterpret_cast<volatile int*>(last_flag) != 0;
+                    bool last = *reinterpret_cast<volatile int*>(last_flag) != 0;
                     epilogue_barrier();
                     if (!last) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_pair(cluster_map(&dempty[buf], 0));
-                        continue;
-                    }
-                }
-                if (warp == kEpilogue0 && lane == 0) atomicExch(counter, 0u);  // all have counted themselves
-                __threadfence();
-            }
-            // A lane holds one channel of 8 tokens; through the warp's buffer it gets 4 neighbouring channels
-            // of one token at a time, so that the outputs and the residual move 8 bytes at a time: LINEAR and
-            // BACKWARD 8 lanes per token (32 channels), GATED 4 (16 channels, gate and up).
-            constexpr int kLanes = MODE == kGated ? 4 : 8, kTok = 32 / kLanes, kIts = kOutCols / kTok;
-            const int ch = 4 * (lane % kLanes), tk = lane / kLanes;
-            const int n = MODE == kGated ? tc * 128 + rank * 64 + 16 * quarter + ch : tc * 256 + rank * 128 + 32 * quarter + ch;
-            const int ld = MODE == kBackward ? p.K : p.N;
-            const bool in = n < ld;  // the last pair's second half may be past N (whole warps)
-            float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (MODE == kLinear && p.bias != nullptr && in) {
-                const uint2 b = *reinterpret_cast<const uint2*>(p.bias + n);
-                bias[0] = __uint_as_float(b.x << 16);
-                bias[1] = __uint_as_float(b.x & 0xFFFF0000u);
-                bias[2] = __uint_as_float(b.y << 16);
-                bias[3] = __uint_as_float(b.y & 0xFFFF0000u);
-            }
-            // the partial tiles of the first two other contributors, fetched one chunk ahead (those after them
-            // are rare)
-            float x0[kOutCols], x1[kOutCols];
-            const float* s0 = part0 + (w.index == 0 ? part_step : 0);
-            const float* s1 = part0 + (w.index <= 1 ? 2 * part_step : part_step);
-            auto fetch = [&](int c0) {
-                if (!w.partial || c0 >= mlim) return;
-#pragma unroll
-                for (int j = 0; j < kOutCols; ++j) x0[j] = __ldcg(s0 + (size_t)(c0 + j) * 128);
-                if (w.count > 2) {
-#pragma unroll
-                    for (int j = 0; j < kOutCols; ++j) x1[j] = __ldcg(s1 + (size_t)(c0 + j) * 128);
-                }
-            };
-            fetch(cb);
+                        float* mine = part0 + w.index * part_step;
 #pragma unroll 1
-            for (int c0 = cb; c0 < mlim; c0 += kOutCols) {
-                const size_t o0 = (size_t)(m0 + c0 + tk) * ld + n;
-                const size_t step = (size_t)kTok * ld;
-                float token[kIts];  // the tokens' scales
+                        for (int c0 = cb; c0 < mlim; c0 += 16) {
+                            uint32_t r[16];
+                            tmem_ld_32x32b_x16(d + (uint32_t)c0, r);
+                            tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < kIts; ++i)
-                    token[i] = MODE == kLinear                ? 1.0f
-                               : c0 + tk + i * kTok < mlim ? __ldcg(p.row_scale + m0 + c0 + tk + i * kTok)
-                                                           : 0.0f;
-                uint2 res[kIts];
-                if (MODE == kLinear && p.residual != nullptr && in) {
-#pragma unroll
-                    for (int i = 0; i < kIts; ++i)
-                        if (c0 + tk + i * kTok < mlim) res[i] = *reinterpret_cast<const uint2*>(p.residual + o0 + i * step);
-                }
-                float acc[kOutCols];
-                {
-                    uint32_t r[kOutCols];
-                    tmem_ld_32x32b_x8(d + (uint32_t)c0, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < kOutCols; ++j) acc[j] = __uint_as_float(r[j]);
-                }
-                if (w.partial) {
-                    float own[kOutCols];
-#pragma unroll
-                    for (int j = 0; j < kOutCols; ++j) {
-                        own[j] = acc[j];
-                        acc[j] = w.index == 0 ? own[j] : x0[j];
-                        acc[j] += w.index == 0 ? x0[j] : w.index == 1 ? own[j] : x1[j];
-                        if (w.count > 2 && w.index <= 1) acc[j] += x1[j];
+                            for (int j = 0; j < 16; ++j) __stcg(mine + (size_t)(c0 + j) * 128, __uint_as_float(r[j]));
+                        }
+                        __threadfence();
+                        epilogue_barrier();
+                        if (warp == kEpilogue0 && lane == 0) *last_flag = atomic_add_acq_rel_gpu(counter, 1u) == others;
+                        epilogue_barrier();
+                        last = *reinterpret_cast<volatile int*>(last_flag) != 0;
+                        epilogue_barrier();
+                        if (!last) continue;
                     }
-                    fetch(c0 + kOutCols);
-#pragma unroll 1
-                    for (int q = 2; q < w.count; ++q) {
-                        if (q == 2 && w.index <= 1) continue;  // added above
+                    if (warp == kEpilogue0 && lane == 0) atomicExch(counter, 0u);  // all have counted themselves
+                    __threadfence();
+                }
+                // A lane holds one channel of 8 tokens; through the warp's buffer it gets 4 neighbouring channels
+                // of one token at a time, so that the outputs and the residual move 8 bytes at a time: LINEAR and
+                // BACKWARD 8 lanes per token (32 channels), GATED 4 (16 channels, gate and up).
+                constexpr int kLanes = MODE == kGated ? 4 : 8, kTok = 32 / kLanes, kIts = kOutCols / kTok;
+                const int ch = 4 * (lane % kLanes), tk = lane / kLanes;
+                const int n = MODE == kGated ? tc * 128 + rank * 64 + 16 * quarter + ch : tc * 256 + rank * 128 + 32 * quarter + ch;
+                const int ld = MODE == kBackward ? p.K : p.N;
+                const bool in = n < ld;  // the last pair's second half may be past N (whole warps)
+                float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (MODE == kLinear && p.bias != nullptr && in) {
+                    const uint2 b = *reinterpret_cast<const uint2*>(p.bias + n);
+                    bias[0] = __uint_as_float(b.x << 16);
+                    bias[1] = __uint_as_float(b.x & 0xFFFF0000u);
+                    bias[2] = __uint_as_float(b.y << 16);
+                    bias[3] = __uint_as_float(b.y & 0xFFFF0000u);
+                }
+                // the partial tiles of the first two other contributors, fetched one chunk ahead (those after them
+                // are rare)
+                float x0[kOutCols], x1[kOutCols];
+                const float* s0 = part0 + (w.index == 0 ? part_step : 0);
+                const float* s1 = part0 + (w.index <= 1 ? 2 * part_step : part_step);
+                auto fetch = [&](int c0) {
+                    if (!w.partial || c0 >= mlim) return;
 #pragma unroll
-                        for (int j = 0; j < kOutCols; ++j)
-                            acc[j] += q == w.index ? own[j] : __ldcg(part0 + q * part_step + (size_t)(c0 + j) * 128);
+                    for (int j = 0; j < kOutCols; ++j) x0[j] = __ldcg(s0 + (size_t)(c0 + j) * 128);
+                    if (w.count > 2) {
+#pragma unroll
+                        for (int j = 0; j < kOutCols; ++j) x1[j] = __ldcg(s1 + (size_t)(c0 + j) * 128);
                     }
-                }
-                __syncwarp();  // the previous columns have left the buffer
-#pragma unroll
-                for (int j = 0; j < kOutCols; ++j) out[j * kOutStride + lane] = acc[j];
-                __syncwarp();
-                float v[4 * kIts];
-#pragma unroll
-                for (int i = 0; i < kIts; ++i) {
-                    const float4 a = *reinterpret_cast<const float4*>(out + (tk + i * kTok) * kOutStride + ch);
-                    v[4 * i] = fmaf(a.x, token[i], bias[0]);
-                    v[4 * i + 1] = fmaf(a.y, token[i], bias[1]);
-                    v[4 * i + 2] = fmaf(a.z, token[i], bias[2]);
-                    v[4 * i + 3] = fmaf(a.w, token[i], bias[3]);
-                }
-                auto put = [&](uint16_t* dst, const float (&f)[4 * kIts]) {
-#pragma unroll
-                    for (int i = 0; i < kIts; ++i)
-                        if (in && c0 + tk + i * kTok < mlim)
-                            *reinterpret_cast<uint2*>(dst + o0 + i * step) =
-                                make_uint2(bf16x2_of(f[4 * i], f[4 * i + 1]), bf16x2_of(f[4 * i + 2], f[4 * i + 3]));
                 };
-                if constexpr (MODE == kGated) {
-                    float u[4 * kIts];
+                fetch(cb);
+#pragma unroll 1
+                for (int c0 = cb; c0 < mlim; c0 += kOutCols) {
+                    const size_t o0 = (size_t)(m0 + c0 + tk) * ld + n;
+                    const size_t step = (size_t)kTok * ld;
+                    float token[kIts];  // the tokens' scales
 #pragma unroll
-                    for (int i = 0; i < kIts; ++i) {
-                        const float4 a = *reinterpret_cast<const float4*>(out + (tk + i * kTok) * kOutStride + 16 + ch);
-                        u[4 * i] = a.x * token[i];
-                        u[4 * i + 1] = a.y * token[i];
-                        u[4 * i + 2] = a.z * token[i];
-                        u[4 * i + 3] = a.w * token[i];
+                    for (int i = 0; i < kIts; ++i)
+                        token[i] = MODE == kLinear                ? 1.0f
+                                   : c0 + tk + i * kTok < mlim ? __ldcg(p.row_scale + m0 + c0 + tk + i * kTok)
+                                                               : 0.0f;
+                    uint2 res[kIts];
+                    if (MODE == kLinear && p.residual != nullptr && in) {
+#pragma unroll
+                        for (int i = 0; i < kIts; ++i)
+                            if (c0 + tk + i * kTok < mlim) res[i] = *reinterpret_cast<const uint2*>(p.residual + o0 + i * step);
                     }
-                    if (p.pre != nullptr) {
-                        put(p.pre, v);
-                        put(p.pre2, u);
+                    float acc[kOutCols];
+                    {
+                        uint32_t r[kOutCols];
+                        tmem_ld_32x32b_x8(d + (uint32_t)c0, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < kOutCols; ++j) acc[j] = __uint_as_float(r[j]);
                     }
-                    act_values(p.act, v);
+                    if (w.partial) {
+                        float own[kOutCols];
 #pragma unroll
-                    for (int i = 0; i < 4 * kIts; ++i) v[i] *= u[i];
-                } else if constexpr (MODE == kLinear) {
-                    if (p.pre != nullptr) put(p.pre, v);
-                    act_values(p.act, v);
-                    if (p.residual != nullptr) {
+                        for (int j = 0; j < kOutCols; ++j) {
+                            own[j] = acc[j];
+                            acc[j] = w.index == 0 ? own[j] : x0[j];
+                            acc[j] += w.index == 0 ? x0[j] : w.index == 1 ? own[j] : x1[j];
+                            if (w.count > 2 && w.index <= 1) acc[j] += x1[j];
+                        }
+                        fetch(c0 + kOutCols);
+#pragma unroll 1
+                        for (int q = 2; q < w.count; ++q) {
+                            if (q == 2 && w.index <= 1) continue;  // added above
 #pragma unroll
-                        for (int i = 0; i < kIts; ++i) {
-                            v[4 * i] += __uint_as_float(res[i].x << 16);
-                            v[4 * i + 1] += __uint_as_float(res[i].x & 0xFFFF0000u);
-                            v[4 * i + 2] += __uint_as_float(res[i].y << 16);
-                            v[4 * i + 3] += __uint_as_float(res[i].y & 0xFFFF0000u);
+                            for (int j = 0; j < kOutCols; ++j)
+                                acc[j] += q == w.index ? own[j] : __ldcg(part0 + q * part_step + (size_t)(c0 + j) * 128);
                         }
                     }
+                    __syncwarp();  // the previous columns have left the buffer
+#pragma unroll
+                    for (int j = 0; j < kOutCols; ++j) out[j * kOutStride + lane] = acc[j];
+                    __syncwarp();
+                    float v[4 * kIts];
+#pragma unroll
+                    for (int i = 0; i < kIts; ++i) {
+                        const float4 a = *reinterpret_cast<const float4*>(out + (tk + i * kTok) * kOutStride + ch);
+                        v[4 * i] = fmaf(a.x, token[i], bias[0]);
+                        v[4 * i + 1] = fmaf(a.y, token[i], bias[1]);
+                        v[4 * i + 2] = fmaf(a.z, token[i], bias[2]);
+                        v[4 * i + 3] = fmaf(a.w, token[i], bias[3]);
+                    }
+                    auto put = [&](uint16_t* dst, const float (&f)[4 * kIts]) {
+#pragma unroll
+                        for (int i = 0; i < kIts; ++i)
+                            if (in && c0 + tk + i * kTok < mlim)
+                                *reinterpret_cast<uint2*>(dst + o0 + i * step) =
+                                    make_uint2(bf16x2_of(f[4 * i], f[4 * i + 1]), bf16x2_of(f[4 * i + 2], f[4 * i + 3]));
+                    };
+                    if constexpr (MODE == kGated) {
+                        float u[4 * kIts];
+#pragma unroll
+                        for (int i = 0; i < kIts; ++i) {
+                            const float4 a = *reinterpret_cast<const float4*>(out + (tk + i * kTok) * kOutStride + 16 + ch);
+                            u[4 * i] = a.x * token[i];
+                            u[4 * i + 1] = a.y * token[i];
+                            u[4 * i + 2] = a.z * token[i];
+                            u[4 * i + 3] = a.w * token[i];
+                        }
+                        if (p.pre != nullptr) {
+                            put(p.pre, v);
+                            put(p.pre2, u);
+                        }
+                        act_values(p.act, v);
+#pragma unroll
+                        for (int i = 0; i < 4 * kIts; ++i) v[i] *= u[i];
+                    } else if constexpr (MODE == kLinear) {
+                        if (p.pre != nullptr) put(p.pre, v);
+                        act_values(p.act, v);
+                        if (p.residual != nullptr) {
+#pragma unroll
+                            for (int i = 0; i < kIts; ++i) {
+                                v[4 * i] += __uint_as_float(res[i].x << 16);
+                                v[4 * i + 1] += __uint_as_float(res[i].x & 0xFFFF0000u);
+                                v[4 * i + 2] += __uint_as_float(res[i].y << 16);
+                                v[4 * i + 3] += __uint_as_float(res[i].y & 0xFFFF0000u);
+                            }
+                        }
+                    }
+                    put(p.y, v);
                 }
-                put(p.y, v);
             }
             tc_fence_before();
             __syncwarp();
@@ -843,21 +849,26 @@ FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms) {
     g.tiles = (int64_t)g.tiles_c * ((M + g.bn - 1) / g.bn);
     const int rest = (int)(g.tiles % g.pairs);
     // Cycles that the last round and the cut tiles add: a stage takes the longer of its MMAs and its
-    // dequant; joining c contributors about (30 bn + 800) c + 3000, which hides behind the whole tiles
-    // that follow the cut ones, if there are any.  Either the rest alone is cut (n runs per tile, at most
-    // one per pair), or the rest and one full round (one run per pair).
+    // dequant; joining c contributors about (30 bn + 800) c + 3000, half of that by halves, which hides
+    // behind the whole tiles that follow the cut ones, if there are any.  Either the rest alone is cut (n
+    // runs per tile, at most one per pair), or the rest and one full round (one run per pair).
     const double stage = std::max(1.45 * g.bn + 130.0, 440.0), tile = 2.0 * entries * stage;
-    auto join = [&](int c, bool hidden) {
-        const double cost = (30.0 * g.bn + 800.0) * c + 3000.0;
+    auto join = [&](int c, bool halves, bool hidden) {
+        const double cost = ((halves ? 15.0 : 30.0) * g.bn + 800.0) * c + (halves ? 4500.0 : 3000.0);
         return hidden ? std::max(0.0, cost - tile) : cost;
     };
+    // By halves pays where every run lies in one tile, so that a tile's contributors end together, with wide
+    // tiles and few contributors (1023 tokens, 5120 x 5120 backward, 4 contributors: 51.7 -> 45.8 us; 300, 4096 x
+    // 4096, 2: 26.1 -> 21.9); elsewhere the second count costs more (20 tokens, 4096 x 4096, 5 contributors: 13.5
+    // -> 15.7 us; 512, 4096 x 14336, 112 tiles in 74 runs: 55.1 -> 60.9).  As many parts as contributors: the same.
+    auto by_halves = [&](int runs, int cut) { return runs % cut == 0 && runs / cut <= 4 && g.bn >= 96; };
     double best = rest > 0 ? tile : 0.0;
     for (int n = 2; rest > 0 && n <= 16; ++n) {
         const int runs = std::min(g.pairs, rest * n);
         const int units = rest * entries;
         if (units / runs < 2) break;
         const int c = runs % rest == 0 ? runs / rest : runs / rest + 2;  // most contributors of a tile
-        const double cost = 2.0 * stage * units / runs + join(c, g.tiles > g.pairs);
+        const double cost = 2.0 * stage * units / runs + join(c, by_halves(runs, rest), g.tiles > g.pairs);
         if (cost < best) {
             best = cost;
             g.cut = rest;
@@ -865,12 +876,13 @@ FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms) {
         }
     }
     if (rest > 0 && g.tiles > g.pairs) {
-        const double cost = tile * rest / g.pairs + join(3, g.tiles > 2 * g.pairs);
+        const double cost = tile * rest / g.pairs + join(3, false, g.tiles > 2 * g.pairs);
         if (cost < best) {
             g.cut = rest + g.pairs;
             g.runs = g.pairs;
         }
     }
+    g.halves = g.cut > 0 && by_halves(g.runs, g.cut);
     g.partial_bytes = (size_t)(g.cut + g.runs) * 2 * 128 * g.bn * 4;
     return g;
 }
@@ -904,6 +916,7 @@ cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnA
     g.tiles = (int)plan.tiles;
     g.cut = plan.cut;
     g.runs = plan.runs;
+    g.halves = plan.halves;
     const bool narrow = plan.bn <= 128;
     auto* fn = back  ? (narrow ? ffn_gemm_kernel<kBackward, true> : ffn_gemm_kernel<kBackward, false>)
                : two ? (narrow ? ffn_gemm_kernel<kGated, true> : ffn_gemm_kernel<kGated, false>)

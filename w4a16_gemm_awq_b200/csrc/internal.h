@@ -209,6 +209,7 @@ struct FfnPlan {
     int tiles_c;     // tiles along the output channels
     int64_t tiles;
     int cut, runs;   // tiles cut along the contraction, and the runs that they are cut into
+    bool halves;     // cut tiles are joined by halves of their columns
     size_t partial_bytes;
 };
 FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms);
@@ -218,7 +219,7 @@ FfnPlan ffn_plan(int64_t M, int rows, int entries, int num_sms);
 struct FfnMaps {
     CUtensorMap x, w, w2;
 };
-// counters: 2 per cut tile, zero between calls.
+// counters: 4 per cut tile, zero between calls.
 cudaError_t launch_ffn_gemm(const FfnMaps& maps, const FfnPlan& plan, const FfnArgs& a, bool back, bool two,
                             float* partials, unsigned* counters, unsigned* err, cudaStream_t stream);
 
