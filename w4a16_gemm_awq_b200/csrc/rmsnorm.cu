@@ -10,9 +10,9 @@
 //   - Many rows: a block walks rows that bulk copies bring into a ring in shared memory, so the loads of
 //     the next rows are in flight whatever the threads do with the current one (loads issued by the
 //     threads themselves, one row at a time: e4m3 1999 x 5120 26.6 us, backward 4096 x 4096 38.8 us;
-//     with the ring 16.4 us and 35.4 us, 4.4 and 3.8 TB/s; 8192 x 8192 in bf16 94 us, 5.7 TB/s of the
-//     6.55 that a copy reaches).  A thread holds 4 chunks of 8 channels of the row, packed as bf16 (the
-//     sum h is exact there), and weight / s.
+//     with the ring 16.4 us and 32.5 us, 4.4 and 4.1 TB/s; 8192 x 8192 in bf16 94 us, 5.7 TB/s of the
+//     6.55 that a copy reaches).  A thread holds 4 chunks of 8 channels of the row (backward 2 or 4),
+//     packed as bf16 (the sum h is exact there), and weight / s.
 //   - Few rows: one block per row with as many threads as it has chunks, which shortens its latency.
 //   - The backward pass runs several rows per block side by side (one group of warps each, with its own
 //     ring and barrier), so that few partial sums of dweight are left.
@@ -542,15 +542,14 @@ struct NormBwdPlan {
     size_t smem;
 };
 
-NormBwdPlan norm_backward_plan(int64_t M, int K, int srcs, int num_sms) {
+// Many rows with V chunks per thread.
+NormBwdPlan norm_backward_many(int64_t M, int K, int srcs, int num_sms, int V) {
     NormBwdPlan b{};
-    const bool many = norm_many(M, num_sms);
-    b.V = many || K > 16384 ? 4 : K > 8192 ? 2 : 1;
-    b.T = norm_threads(K, b.V);
-    b.groups = many && b.T <= 256 ? (512 / b.T < 8 ? 512 / b.T : 8) : 1;
+    b.V = V;
+    b.T = norm_threads(K, V);
+    b.groups = b.T <= 256 ? (512 / b.T < 8 ? 512 / b.T : 8) : 1;
     const int64_t need = (M + b.groups - 1) / b.groups;
     b.grid = (int)(need < num_sms ? need : num_sms);
-    if (!many) return b;
     const size_t row = (size_t)2 * K * srcs;
     // at least two rows: one is filled while the other is read
     while (b.groups > 1 && 2 * b.groups * row > kRingBytes) --b.groups;
@@ -561,9 +560,31 @@ NormBwdPlan norm_backward_plan(int64_t M, int K, int srcs, int num_sms) {
     return b;
 }
 
+NormBwdPlan norm_backward_plan(int64_t M, int K, int srcs, int num_sms) {
+    if (norm_many(M, num_sms)) {
+        // Four chunks; two where four leave each group one row ahead of the one it reads and two leave no
+        // fewer threads: fewer groups, each with more rows on their way (4096 rows with dh: K 4096 33.9 -> 31.1
+        // us, K 8192 55.4 -> 53.5; without dh, three rows per group: K 4096 25.7 -> 28.2, K 8192 39 -> 47; K
+        // 5120 with dh, 320 threads instead of 480: 40.6 -> 45.2).
+        const NormBwdPlan b = norm_backward_many(M, K, srcs, num_sms, 4);
+        if (b.depth != 2) return b;
+        const NormBwdPlan c = norm_backward_many(M, K, srcs, num_sms, 2);
+        return c.depth > 2 && c.T <= 512 && c.T * c.groups >= b.T * b.groups ? c : b;
+    }
+    NormBwdPlan b{};
+    b.V = K > 16384 ? 4 : K > 8192 ? 2 : 1;
+    b.T = norm_threads(K, b.V);
+    b.groups = 1;
+    b.grid = (int)(M < num_sms ? M : num_sms);
+    return b;
+}
+
 }  // namespace
 
-int rmsnorm_backward_rows(int64_t M, int K, int num_sms) { return norm_backward_plan(M, K, 3, num_sms).grid; }
+int rmsnorm_backward_rows(int64_t M, int K, int num_sms) {
+    const int a = norm_backward_plan(M, K, 2, num_sms).grid, b = norm_backward_plan(M, K, 3, num_sms).grid;
+    return a > b ? a : b;
+}
 
 cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
                            float eps, uint16_t* h, uint16_t* y, uint8_t* q, float* scales, int group, int64_t M, int K,
@@ -582,12 +603,14 @@ cudaError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const
     const size_t sums = (size_t)(b.groups - 1) * K * 4;
     const size_t smem = b.smem > sums ? b.smem : sums;
     const bool exact = K == 8 * b.V * b.T;
-    auto* fn = b.depth > 0 ? (threads > 512 ? rmsnorm_backward_kernel<4, 1024, true, false>
-                              : exact       ? rmsnorm_backward_kernel<4, 512, true, true>
-                                            : rmsnorm_backward_kernel<4, 512, true, false>)
-               : b.V == 1  ? rmsnorm_backward_kernel<1, 1024, false, false>
-               : b.V == 2  ? rmsnorm_backward_kernel<2, 1024, false, false>
-                           : rmsnorm_backward_kernel<4, 1024, false, false>;
+    auto* fn = b.depth > 0 && b.V == 2 ? (exact ? rmsnorm_backward_kernel<2, 512, true, true>
+                                                : rmsnorm_backward_kernel<2, 512, true, false>)
+               : b.depth > 0           ? (threads > 512 ? rmsnorm_backward_kernel<4, 1024, true, false>
+                                          : exact       ? rmsnorm_backward_kernel<4, 512, true, true>
+                                                        : rmsnorm_backward_kernel<4, 512, true, false>)
+               : b.V == 1              ? rmsnorm_backward_kernel<1, 1024, false, false>
+               : b.V == 2              ? rmsnorm_backward_kernel<2, 1024, false, false>
+                                       : rmsnorm_backward_kernel<4, 1024, false, false>;
     cudaError_t e;
     if (smem > 32 * 1024) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
