@@ -262,3 +262,34 @@ def test_small_workspaces_are_refused():
             with pytest.raises(w4.W4A16Error):
                 f(torch.zeros(size, dtype=torch.uint8, device="cuda"))
     w4.check_device_status()
+
+
+def test_cut_tiles_repeat():
+    """Tiles cut along the contraction, few wide ones joined by halves, many narrow ones whole: the bits of
+    fifty calls agree, two streams at once included, and the counters are zero afterwards."""
+    one = [(cuda(ref.pack_layer(1, 384, 14336)[0]), 14336, 384), (cuda(ref.pack_layer(2, 4096, 1024)[0]), 1024, 4096),
+           (cuda(ref.pack_layer(3, 256, 8192)[0]), 8192, 256)]
+    up = cuda(ref.pack_layer(4, 256, 8192)[0])
+    calls = []
+    for M in (20, 64, 100, 130, 250, 300):
+        for layer, K, N in one:
+            x, dy = ref.bf(M, M, K).cuda(), ref.bf(M + 1, M, N).cuda()
+            calls.append((w4.OP_LINEAR, M, N, K, lambda ws, x=x, w=layer: w4.w4a16_linear_fused(x, *w, workspace=ws)))
+            calls.append((w4.OP_LINEAR_BACKWARD, M, N, K,
+                          lambda ws, dy=dy, w=layer: w4.w4a16_linear_fused_backward(dy, *w, workspace=ws)[0]))
+        calls.append((w4.OP_GATED, M, N, K, lambda ws, x=x, w=layer: w4.w4a16_gated(x, w, up, workspace=ws)))
+    need = max(w4.w4a16_fused_workspace_bytes(*c[:4]) for c in calls)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.zeros(need, dtype=torch.uint8, device="cuda") for _ in streams]
+    for *_, f in calls:
+        want = f(spaces[0]).clone()
+        torch.cuda.synchronize()
+        outs = []
+        for _ in range(25):
+            for st, ws in zip(streams, spaces):
+                with torch.cuda.stream(st):
+                    outs.append(f(ws))
+        torch.cuda.synchronize()
+        assert all(torch.equal(bits(o), bits(want)) for o in outs)
+    w4.check_device_status()
+    assert not any(ws[:131072].any() for ws in spaces)

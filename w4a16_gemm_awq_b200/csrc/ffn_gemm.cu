@@ -37,8 +37,9 @@
 //     lanes l and l + 16 and meet by a shuffle.
 //   - Whole tiles go round the pairs; the tiles that do not fill a round are cut along the contraction
 //     into equal runs, one per pair, whose fp32 partial tiles meet in the workspace: the last to arrive
-//     adds them in the order of the runs, so the bits do not depend on which that is.  The cut tiles
-//     come first, so that joining them hides behind whole tiles.  No pair waits for another.
+//     (at a half of the columns, where the contributors end together) adds them in the order of the runs,
+//     so the bits do not depend on which that is.  The cut tiles come first, so that joining them hides
+//     behind whole tiles.  No pair waits for another.
 //   - Bound: with many tokens the tensor pipe, 96 % busy (4096 tokens, K 4096, F 14336: 598 us alone, 1.61
 //     PFLOP/s; 706 to 742 us in a row of calls, at the clock that the power limit leaves).  With few, the
 //     loads and the dequant, about as long as one another (32 tokens, 16384 x 18944: 61 us, 2.5 TB/s of
