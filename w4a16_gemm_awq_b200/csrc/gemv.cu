@@ -560,6 +560,9 @@ gemv_w4a16_kernel(const __grid_constant__ GemvKernelMaps<EPI> maps, const GemvAr
                             wv[gg][i][hh] = make_uint4(s3[0], s3[1], s3[2], 0u);
                         }
                     }
+            // the refill writes the slot through the async proxy, which only this fence orders behind reads that
+            // are still in flight
+            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&wempty[slot]);
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(&xfull[slot], (s / S) & 1))) {
@@ -749,7 +752,9 @@ gemv_w4a16_kernel(const __grid_constant__ GemvKernelMaps<EPI> maps, const GemvAr
                 }
             }
             if (seg + 1 < nseg) {
-                // ready for the next row block's rows; tell every sender its rows were summed
+                // ready for the next row block's rows; tell every sender its rows were summed (the senders' bulk
+                // copies write them through the async proxy)
+                fence_proxy_async_smem();
                 if (lane == 0) mbar_arrive_expect_tx(cready, recv_bytes);
                 for (int q = 0; q < cl; ++q)
                     if (q != (int)crank) mbar_arrive_cluster(cluster_map(cdone, (uint32_t)q));
