@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(512) linear_dp_kernel(const uint16_t* dy, cons
                 }
             }
         }
+        fence_proxy_async_smem();  // this thread's reads of the slot, before its refill
         const int e = token_exponent(block_max(mx, buf), 14);
         const long long next = m + (long long)depth * gridDim.x;  // every thread has its part of the row
         if (threadIdx.x == 0 && next < M) load_row(slot, next);
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(512) gated_dp_kernel(const uint16_t* dh, const
                 largest(x[0], y[0]);
             }
         }
+        if constexpr (KEEP) fence_proxy_async_smem();  // this thread's reads of the slot, before its refill
         const int e = token_exponent(block_max(mx, buf), 14);
         if constexpr (KEEP) {  // every thread has its part of the row
             const long long next = m + (long long)depth * gridDim.x;

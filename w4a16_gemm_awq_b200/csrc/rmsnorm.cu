@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const NormArgs p) {
                 if (shared_max && (t & 15) == 0 && (FULL || (c * T + t) * 8 < K)) atomicMax(&gmax[flip][group[c]], u);
             }
         }
+        if constexpr (RING) fence_proxy_async_smem();  // this thread's reads of the slot, before its refill
         group_sum<1>(ss, buf[flip], t, T, 1);
         if constexpr (RING) {  // every thread has its part of the row: the slot takes the row `depth` further on
             const long long next = m + (long long)p.depth * gridDim.x;
@@ -416,6 +417,7 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_backward_kernel(const NormBwdArg
             }
         }
         if constexpr (RING) {
+            fence_proxy_async_smem();  // this thread's reads of the slot, before its refill
             if (++slot == p.depth) {
                 slot = 0;
                 phase ^= 1;
