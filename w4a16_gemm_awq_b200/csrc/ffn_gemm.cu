@@ -223,12 +223,23 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Arrive on a barrier of either CTA of the pair.  What it announces is either in the async proxy's view
-// already (the writers' proxy fence) or in TMEM (tcgen05 fences), so CTA-scope release is enough; the
-// cluster-scope form costs a memory barrier per stage (gated, 4096 tokens, K 4096, F 14336: 1444 us
-// with it, 1122 us without, before the changes that came after).
-__device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrivals on the leader's barriers from either CTA of the pair; what one CTA of the pair does for the other is
+// waited for with acquire at cluster scope.  mbar_arrive_written releases this CTA's shared memory (the A stage,
+// which its writers have passed to the async proxy) at cluster scope and nothing else: a release of all memory is
+// a barrier behind the SM's global accesses too (gated, 4096 tokens, K 4096, F 14336: 1394 us with it, 707 us
+// without any).  This one takes 4 us of 63 at 32 tokens, 16384 x 18944, 1 of 28 at 77, 8192 x 8192, and nothing of
+// the long products.  mbar_arrive_read needs no release: the reads of an accumulator are ordered by the tcgen05
+// fences on both sides.
+__device__ __forceinline__ void mbar_arrive_written(uint32_t bar) {
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
+        ::"r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_read(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // w & MASK over the bits of MAGIC.
@@ -304,17 +315,25 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // The whole warp waits for a barrier phase, bounded in time.  Every branch goes by a vote, so the lanes
-// stay converged, as the .aligned instructions after a wait require.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+// stay converged, as the .aligned instructions after a wait require.  CLUSTER: a phase on which the other CTA
+// arrives too; acquires at cluster scope.
+template <bool CLUSTER>
+__device__ __forceinline__ bool warp_wait_in(uint64_t* bar, uint32_t parity) {
+    auto done = [&]() {
+        return __all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) != 0;
+    };
+    if (done()) return true;
     const unsigned long long t0 = global_timer_ns();
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
-            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+            if (done()) return true;
         if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kWaitLimitNs)) return false;
     }
 }
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) { return warp_wait_in<false>(bar, parity); }
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) { return warp_wait_in<true>(bar, parity); }
 
 // Barrier among the epilogue warps.
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -459,7 +478,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             const int m0 = (w.tile / p.tiles_c) * p.bn + rank * half_bn;
             for (int c = 2 * w.e0; c < 2 * w.e1; ++c, ++s) {
                 const unsigned slot = s % kS;
-                if (s >= kS && !warp_wait(&empty[slot], (s / kS - 1) & 1)) {
+                if (s >= kS && !warp_wait_cluster(&empty[slot], (s / kS - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -471,7 +490,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             }
         }
         // every MMA has read its stage and said so in both CTAs before either may leave
-        for (unsigned i = s > kS ? s - kS : 0; ok && i < s; ++i) ok = warp_wait(&empty[i % kS], (i / kS) & 1);
+        for (unsigned i = s > kS ? s - kS : 0; ok && i < s; ++i) ok = warp_wait_cluster(&empty[i % kS], (i / kS) & 1);
         if (!ok && lane == 0) fail();
     } else if (warp == 2 || warp == 3) {
         // ---------------------------------------------------------------- packed weights
@@ -506,13 +525,13 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             for (; ok && walk_step(w, p, pair, pairs); ++t) {
                 const unsigned buf = t & 1;
                 const uint32_t d = tmem + buf * kTmemSecond;
-                if (t >= 2 && !warp_wait(&dempty[buf], (t / 2 - 1) & 1)) {
+                if (t >= 2 && !warp_wait_cluster(&dempty[buf], (t / 2 - 1) & 1)) {
                     ok = false;
                     break;
                 }
                 const int stages = 2 * (w.e1 - w.e0);
                 for (int c = 0; c < stages; ++c) {
-                    if (!warp_wait(&full[slot], phase)) {
+                    if (!warp_wait_cluster(&full[slot], phase)) {
                         ok = false;
                         break;
                     }
@@ -533,11 +552,11 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 }
             }
             // the other CTA's last arrivals are here before this one may leave
-            for (unsigned i = t > 2 ? t - 2 : 0; ok && i < t; ++i) ok = warp_wait(&dempty[i & 1], (i / 2) & 1);
+            for (unsigned i = t > 2 ? t - 2 : 0; ok && i < t; ++i) ok = warp_wait_cluster(&dempty[i & 1], (i / 2) & 1);
             if (!ok) {
                 if (lane == 0) fail();
                 if (elect_one()) commit_pair(drain);  // MMAs in flight finish first
-                (void)warp_wait(drain, 0);
+                (void)warp_wait_cluster(drain, 0);
             }
         }
     } else if (warp >= kDequant0) {
@@ -603,7 +622,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                     }
                 }
                 const unsigned s = 2 * (unsigned)i + h, slot = s % kS;
-                if (s >= kS && !warp_wait(&empty[slot], (s / kS - 1) & 1)) {
+                if (s >= kS && !warp_wait_cluster(&empty[slot], (s / kS - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -614,7 +633,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                         weights(c < 4 ? u4_get(cur.a, c) : u4_get(cur.b, c - 4));
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_pair(cluster_map(&full[slot], 0));
+                if (lane == 0) mbar_arrive_written(cluster_map(&full[slot], 0));
                 cur = next;
             }
         }
@@ -647,7 +666,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         bool ok = true;
         for (unsigned t = 0; walk_step(w, p, pair, pairs); ++t) {
             const unsigned buf = t & 1;
-            if (!warp_wait(&dfull[buf], (t / 2) & 1)) {
+            if (!warp_wait_cluster(&dfull[buf], (t / 2) & 1)) {
                 ok = false;
                 break;
             }
@@ -830,7 +849,7 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair(cluster_map(&dempty[buf], 0));
+            if (lane == 0) mbar_arrive_read(cluster_map(&dempty[buf], 0));
         }
         if (!ok && lane == 0) fail();
     }
