@@ -44,8 +44,9 @@
 //     PFLOP/s; 706 to 742 us in a row of calls, at the clock that the power limit leaves).  With few, the
 //     loads and the dequant, about as long as one another (32 tokens, 16384 x 18944: 61 us, 2.5 TB/s of
 //     packed weights; 56 us with the dequant's arithmetic left out).
-//   - Every wait is bounded; one that runs out records kErrTimeout and its role stops.  All roles of
-//     both CTAs then meet at the closing cluster barrier, since each of their waits is bounded too.
+//   - Every wait on an mbarrier is bounded; one that runs out records kErrTimeout and its role stops.  The
+//     epilogue warps, which also meet at a barrier of their own, stop together.  All roles of both CTAs then
+//     meet at the closing cluster barrier.
 #include <algorithm>
 #include <cmath>
 
@@ -337,6 +338,17 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity
 
 // Barrier among the epilogue warps.
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// The same, and whether all of them came with true.
+__device__ __forceinline__ bool epilogue_all(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
 
 template <int MODE, bool NARROW>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
@@ -666,10 +678,11 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         bool ok = true;
         for (unsigned t = 0; walk_step(w, p, pair, pairs); ++t) {
             const unsigned buf = t & 1;
-            if (!warp_wait_cluster(&dfull[buf], (t / 2) & 1)) {
-                ok = false;
-                break;
-            }
+            ok = warp_wait_cluster(&dfull[buf], (t / 2) & 1);
+            // The warps meet at barriers over a cut tile, so there all of them go on or none does: a completion
+            // near the limit is seen by some of their waits only.
+            if (w.partial) ok = epilogue_all(ok);
+            if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + t_lane + buf * kTmemSecond;
             const int tc = w.tile % p.tiles_c;
