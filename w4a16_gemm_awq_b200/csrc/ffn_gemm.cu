@@ -521,6 +521,10 @@ ffn_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             }
         }
         if (!ok && lane == 0) fail();
+        // The copies that this warp started must land before the CTA may leave, also where their readers gave up.  A
+        // wait that runs out gave them that time.
+        for (unsigned j = i > kP ? i - kP : 0; j < i && warp_wait(&pfull[j % kP], (j / kP) & 1); ++j) {
+        }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issue
         if (rank == 0) {
