@@ -424,7 +424,7 @@ cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* 
     if (N <= kDpLongest) {
         const int V = N <= 4096 ? 1 : N <= 8192 ? 2 : 4, threads = (N / (8 * V) + 31) / 32 * 32;
         const size_t row = (size_t)2 * N * (act == W4A16_ACT_NONE ? 1 : 2);
-        const size_t ring = N <= 8192 ? 100 * 1024 : 200 * 1024;
+        const size_t ring = N <= 8192 ? kRingSmemBytes / 2 : kRingSmemBytes;
         const int depth = row * kDpDepth <= ring ? kDpDepth : (int)(ring / row);
         const size_t smem = depth * row;
         using Kernel = void (*)(const uint16_t*, const uint16_t*, uint16_t*, float*, float*, long long, int, int, unsigned*);
@@ -440,10 +440,8 @@ cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* 
             default: return cudaErrorInvalidValue;
         }
 #undef W4A16_DP
-        if (smem > 32 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-        }
+        const cudaError_t e = allow_ring_smem(fn);
+        if (e != cudaSuccess) return e;
         if (sums != nullptr) *sum_rows = runs;
         return launch_after(fn, dim3(runs), threads, smem, stream, dy, pre, dp, row_scale, sums, (long long)M, N, depth, err);
     }
@@ -467,7 +465,7 @@ cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_
     const bool keep = F <= 16384;  // 512 threads with four chunks each
     const int threads = keep ? (F / 32 + 31) / 32 * 32 : 512;
     // resident blocks by registers (128 a thread at most), and at least two rows in flight for each
-    constexpr size_t kRing = 200 * 1024;
+    constexpr size_t kRing = kRingSmemBytes;
     const size_t row = (size_t)6 * F;
     int blocks = 512 / threads > 8 ? 8 : 512 / threads;
     while (keep && blocks > 1 && 2 * blocks * row > kRing) --blocks;
@@ -490,8 +488,8 @@ cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_
         default: return cudaErrorInvalidValue;
     }
 #undef W4A16_DP
-    if (smem > 32 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (keep) {
+        const cudaError_t e = allow_ring_smem(fn);
         if (e != cudaSuccess) return e;
     }
     return launch_after(fn, dim3(grid), threads, smem, stream, dh, g, u, dp, row_scale, (long long)M, F, depth, err);

@@ -164,6 +164,16 @@ cudaError_t launch_gemm(const GemmMaps& maps, const GemmPlan& plan, int group_ra
 
 // ------------------------------------------------------------------ feed-forward operators --
 
+// Most dynamic shared memory of the kernels that bring rows through a ring.
+constexpr size_t kRingSmemBytes = 200 * 1024;
+
+// Allows a kernel instance that much.  The limit is state of the function on the device, so it is the same for every
+// call: a host thread that set what its own call needs could lower it between another's setting and launch.
+template <typename Fn>
+inline cudaError_t allow_ring_smem(Fn fn) {
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingSmemBytes);
+}
+
 // y = bf16(v) (q == nullptr), or q and scales per `group` channels (y == nullptr); see rmsnorm.cu.
 cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
                            float eps, uint16_t* h, uint16_t* y, uint8_t* q, float* scales, int group, int64_t M, int K,

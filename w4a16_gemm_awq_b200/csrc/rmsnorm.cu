@@ -488,7 +488,7 @@ int norm_threads(int K, int V) { return up32((K + 8 * V - 1) / (8 * V)); }
 // Many rows: enough that each SM walks several.
 bool norm_many(int64_t M, int num_sms) { return M > 2 * num_sms; }
 
-constexpr size_t kRingBytes = 200 * 1024;  // ring memory of an SM
+constexpr size_t kRingBytes = kRingSmemBytes;  // ring memory of an SM
 
 // Forward launch.
 struct NormPlan {
@@ -518,8 +518,8 @@ NormPlan norm_plan(int64_t M, int K, int srcs, int num_sms) {
 template <int V, int MAXT, bool Q8, bool RING>
 cudaError_t norm_launch(const NormArgs& a, const NormPlan& b, cudaStream_t stream) {
     auto* fn = a.K == 8 * V * b.T ? rmsnorm_kernel<V, MAXT, Q8, RING, true> : rmsnorm_kernel<V, MAXT, Q8, RING, false>;
-    if (b.smem > 32 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)b.smem);
+    if (RING) {
+        const cudaError_t e = allow_ring_smem(fn);
         if (e != cudaSuccess) return e;
     }
     fn<<<b.grid, b.T, b.smem, stream>>>(a);
@@ -614,8 +614,8 @@ cudaError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const
                : b.V == 2              ? rmsnorm_backward_kernel<2, 1024, false, false>
                                        : rmsnorm_backward_kernel<4, 1024, false, false>;
     cudaError_t e;
-    if (smem > 32 * 1024) {
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (b.depth > 0) {
+        e = allow_ring_smem(fn);
         if (e != cudaSuccess) return e;
     }
     fn<<<b.grid, threads, smem, stream>>>(a, b.T);
