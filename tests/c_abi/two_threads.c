@@ -2,11 +2,14 @@
  * Two host threads call the same operators at different widths, each with its own stream, operands and
  * workspace, and count the calls that are refused.  The kernels behind them are the same instances with
  * different amounts of dynamic shared memory.  Prints "ok" when no call was refused.
+ *   two_threads            the norms and the backward passes, at two widths
+ *   two_threads quantize   the quantizer, at two group sizes
  */
 #include <cuda_runtime.h>
 #include <pthread.h>
 #include <stdint.h>
 #include <stdio.h>
+#include <string.h>
 
 #include "w4a16.h"
 
@@ -70,17 +73,46 @@ static void* run(void* arg) {
     return NULL;
 }
 
-int main(void) {
-    work works[2] = {{8192, 0}, {4096 + 1024, 0}};
+static void* quantize(void* arg) {
+    work* w = (work*)arg; /* width: the group size */
+    const int64_t n = 128, k = 32768;
+    cudaStream_t stream;
+    float* weights = (float*)device_zeros((size_t)(n * k) * 4);
+    float* act = (float*)device_zeros((size_t)k * 4);
+    uint32_t* qweight = (uint32_t*)device_zeros((size_t)(n * k) / 2);
+    uint16_t* scales = (uint16_t*)device_zeros((size_t)(n * (k / 128)) * 2);
+    uint32_t* zeros = (uint32_t*)device_zeros((size_t)(n * (k / 128)) / 2);
+    float* s = (float*)device_zeros((size_t)k * 4);
+    int i;
+    w->refused = -1;
+    if (!weights || !act || !qweight || !scales || !zeros || !s) return NULL;
+    if (cudaStreamCreateWithFlags(&stream, cudaStreamNonBlocking) != cudaSuccess) return NULL;
+    if (cudaDeviceSynchronize() != cudaSuccess) return NULL;
+    w->refused = 0;
+    for (i = 0; i < CALLS; ++i) {
+        w->refused += awq_quantize(weights, act, 0.5f, n, k, w->width, qweight, scales, zeros, s, stream) != W4A16_OK;
+        if (i % 100 == 99 && cudaStreamSynchronize(stream) != cudaSuccess) w->refused += 1;
+    }
+    if (cudaStreamSynchronize(stream) != cudaSuccess) w->refused += 1;
+    return NULL;
+}
+
+int main(int argc, char** argv) {
+    const int quantizes = argc > 1 && strcmp(argv[1], "quantize") == 0;
+    work works[2] = {{8192, 0}, {5120, 0}};
     pthread_t threads[2];
     int i;
+    if (quantizes) {
+        works[0].width = 32768;
+        works[1].width = 2048;
+    }
     if (cudaSetDevice(0) != cudaSuccess) return 2;
     for (i = 0; i < 2; ++i)
-        if (pthread_create(&threads[i], NULL, run, &works[i]) != 0) return 2;
+        if (pthread_create(&threads[i], NULL, quantizes ? quantize : run, &works[i]) != 0) return 2;
     for (i = 0; i < 2; ++i) pthread_join(threads[i], NULL);
     if (w4a16_check_device_status(NULL) != W4A16_OK) return 3;
     if (works[0].refused != 0 || works[1].refused != 0) {
-        printf("refused: %d and %d of %d calls each\n", works[0].refused, works[1].refused, 4 * CALLS);
+        printf("refused: %d and %d of %d calls each\n", works[0].refused, works[1].refused, (quantizes ? 1 : 4) * CALLS);
         return 1;
     }
     puts("ok");

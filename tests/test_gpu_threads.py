@@ -69,8 +69,10 @@ def test_two_widths(calls, widths):
 
 @pytest.mark.skipif(shutil.which("gcc") is None or not os.path.exists(os.path.join(CUDA, "include", "cuda_runtime.h")),
                     reason="no host C compiler or no CUDA toolkit headers")
-def test_two_widths_from_c(tmp_path):
-    """The same from a C program, whose threads are inside the library at the same time."""
+@pytest.mark.parametrize("what", ["operators", "quantize"])
+def test_two_widths_from_c(tmp_path, what):
+    """The same from a C program, whose threads are inside the library at the same time; and the quantizer, at two
+    group sizes."""
     lib_dir = os.path.dirname(w4.build())
     out, lib64 = str(tmp_path / "two_threads"), os.path.join(CUDA, "lib64")
     r = subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pthread", "-I", os.path.join(ROOT, "include"),
@@ -78,5 +80,5 @@ def test_two_widths_from_c(tmp_path):
                         "-L", lib_dir, "-lw4a16", "-L", lib64, "-lcudart", f"-Wl,-rpath,{lib_dir}", f"-Wl,-rpath,{lib64}",
                         "-o", out], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout + r.stderr
-    r = subprocess.run([out], capture_output=True, text=True, timeout=300)
+    r = subprocess.run([out, what], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr

@@ -390,8 +390,9 @@ cudaError_t launch_awq_quantize(const float* W, const float* act, float alpha, i
         return cudaErrorInvalidValue;
     if (gs > 1024) {
         const int smem = gs * 4;
+        // the same limit for every call: it is state of the function, which another host thread may set meanwhile
         cudaError_t e = cudaFuncSetAttribute(awq_quantize_large_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             smem);
+                                             kQuantMaxLargeGroup * 4);
         if (e != cudaSuccess) return e;
         dim3 grid(K / gs, (N + kLargeRows - 1) / kLargeRows);
         awq_quantize_large_kernel<<<grid, kQuantThreads, smem, stream>>>(W, act, alpha, N, K, gs, qweight, scales,
