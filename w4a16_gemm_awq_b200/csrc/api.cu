@@ -887,6 +887,7 @@ w4a16_status awq_fold_activations(const uint16_t* x, const float* s, uint16_t* x
 size_t w4a16_fused_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
     if (op < W4A16_OP_LINEAR || op > W4A16_OP_RMSNORM_BACKWARD) return 0;
     if (op == W4A16_OP_RMSNORM_BACKWARD ? validate_norm(M, K, 0.0f) != W4A16_OK : !valid_layer_shape(M, N, K)) return 0;
+    if ((op == W4A16_OP_GATED || op == W4A16_OP_GATED_BACKWARD) && N > kMaxN / 2) return 0;  // 2 F rows
     DeviceInfo* d = nullptr;
     if (device_info(&d) != W4A16_OK) return 0;
     return fused_bytes(op, M, N, K, d->num_sms);
