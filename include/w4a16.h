@@ -499,8 +499,8 @@ w4a16_status w4a16_linear_fused(const uint16_t* x, const w4a16_weights* weights,
  *   dy        [M][N] bf16 bits (also the residual's gradient).
  *   pre       [M][N] bf16 bits, as the forward call wrote it.  Ignored, may be NULL, for NONE.
  *   dx        [M][K] bf16 bits, output.  dbias [N] fp32, output, or NULL.
- *   dp enters the product in fp16 over a power of two per token, its largest value at 2^13 or
- *   more, and each weight rounded once to fp16: |(q - z) scale| <= 65504, or it is infinite.
+ *   dp enters the product in fp16 over a power of two per token, its largest value at 2^14 or
+ *   more (2^-96 or more before the scaling; smaller rows keep fewer bits), and each weight rounded once to fp16: |(q - z) scale| <= 65504, or it is infinite.
  *   dbias sums the unrounded fp32 dp.
  *   workspace: required, W4A16_OP_LINEAR_BACKWARD.  Repeated calls give the same bits.
  *   Errors: as w4a16_linear_fused.

@@ -2,8 +2,8 @@
 // steps of the backward passes.
 //
 // The products' operand is fp16 with a scale per token: x' = fp16(x 2^-e), e such that the token's
-// largest |x'| lies in [2^14, 2^15) (backward: the largest |dy| in [2^13, 2^14), and |act'| <= 1.13).
-// bf16 values keep all their 8 bits down to 2^-28 of the token's largest one, and below that an error
+// largest |x'| lies in [2^14, 2^15); backward, x is the gradient behind the activation's derivative.  bf16
+// values keep all their 8 bits down to 2^-28 of the token's largest one, and below that an error
 // of at most 2^-39 of it is left, under the fp32 sums' own; gradients are rounded to 11 bits.
 //
 // Memory bound: 16-byte loads and stores, each row read from device memory once (a second pass over a
@@ -77,9 +77,9 @@ __device__ __forceinline__ void stream_order() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// One block per row: row_scale[m] = 2^e, and out = fp16(x 2^-e) unless out is nullptr.
+// One block per row: row_scale[m] = 2^e and out = fp16(x 2^-e).
 __global__ void __launch_bounds__(256) half_rows_kernel(const uint16_t* x, uint16_t* out, float* row_scale, long long M,
-                                                        int K, int top) {
+                                                        int K) {
     __shared__ uint32_t buf[32];
     stream_order();
     constexpr int V = 4;  // chunks of a row that stay in registers
@@ -97,9 +97,8 @@ __global__ void __launch_bounds__(256) half_rows_kernel(const uint16_t* x, uint1
         }
         for (int k = (V * 256 + threadIdx.x) * 8; k < K; k += 2048) mx = max_abs8(*reinterpret_cast<const uint4*>(row + k), mx);
         mx = block_max(max(mx & 0xFFFFu, mx >> 16), buf);
-        const int e = token_exponent(mx << 16, top);
+        const int e = token_exponent(mx << 16, 14);
         if (threadIdx.x == 0) row_scale[m] = exp2_int(e);
-        if (out == nullptr) continue;
         const float s = exp2_int(-e);
         auto put = [&](const uint4& v, int k) {
             float f[8];
@@ -117,8 +116,35 @@ __global__ void __launch_bounds__(256) half_rows_kernel(const uint16_t* x, uint1
     }
 }
 
+// One block per row: row_scale[m] = 2^e for dp = dy * act'(pre).  The largest dp may be far below the largest dy, whose
+// unit may be a dead one.
+template <int ACT>
+__global__ void __launch_bounds__(512) dp_scale_kernel(const uint16_t* dy, const uint16_t* pre, float* row_scale, long long M,
+                                                       int N) {
+    __shared__ uint32_t buf[32];
+    stream_order();
+    for (long long m = blockIdx.x; m < M; m += gridDim.x) {
+        uint32_t mx = 0u;
+#pragma unroll 4
+        for (int k = threadIdx.x * 8; k < N; k += 512 * 8) {
+            float v[8];
+            unpack8(*reinterpret_cast<const uint4*>(dy + m * N + k), v);
+            if constexpr (ACT != W4A16_ACT_NONE) {
+                float p[8];
+                unpack8(*reinterpret_cast<const uint4*>(pre + m * N + k), p);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= act_grad<ACT>(p[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx = max(mx, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        }
+        const int e = token_exponent(block_max(mx, buf), 14);
+        if (threadIdx.x == 0) row_scale[m] = exp2_int(e);
+    }
+}
+
 // Rows too long for linear_dp_kernel's registers: dp = fp16(dy * act'(pre) / row_scale), with the scales from
-// half_rows_kernel, over `rows` rows per block.  sums: [gridDim.y][N], nullptr without a bias gradient.
+// dp_scale_kernel, over `rows` rows per block.  sums: [gridDim.y][N], nullptr without a bias gradient.
 template <int ACT>
 __global__ void __launch_bounds__(32 * kDpRowThreads) linear_dp_long_kernel(const uint16_t* dy, const uint16_t* pre,
                                                                             uint16_t* dp, const float* row_scale,
@@ -166,8 +192,7 @@ constexpr int kDpDepth = 4;
 // dp = fp16(dy * act'(pre) / row_scale), one row per block at a time, V chunks of 8 columns per thread.  Rows
 // come through a ring of `depth` as in gated_dp_kernel; a row's values and the block's column sums stay in
 // registers.  sums: [gridDim.x][N], nullptr without a bias gradient.  (1023 x 5120 with GELU: 13 us from
-// device memory; the two kernels for longer rows, of which the first reads dy for the scales, take 17 us
-// and that read.)
+// device memory; the second of the two kernels for longer rows alone takes 17 us.)
 template <int ACT, int V>
 __global__ void __launch_bounds__(512) linear_dp_kernel(const uint16_t* dy, const uint16_t* pre, uint16_t* dp,
                                                         float* row_scale, float* sums, long long M, int N, int depth,
@@ -413,7 +438,7 @@ cudaError_t launch_after(void (*fn)(Args...), dim3 grid, int threads, size_t sme
 cudaError_t launch_half_rows(const uint16_t* x, uint16_t* out, float* row_scale, int64_t M, int K, int num_sms,
                              cudaStream_t stream) {
     return launch_after(half_rows_kernel, dim3(row_blocks(M, num_sms)), 256, 0, stream, x, out, row_scale, (long long)M,
-                        K, 14);
+                        K);
 }
 
 cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* dp, float* row_scale, float* sums,
@@ -445,17 +470,26 @@ cudaError_t launch_linear_dp(const uint16_t* dy, const uint16_t* pre, uint16_t* 
         if (sums != nullptr) *sum_rows = runs;
         return launch_after(fn, dim3(runs), threads, smem, stream, dy, pre, dp, row_scale, sums, (long long)M, N, depth, err);
     }
-    const cudaError_t e = launch_after(half_rows_kernel, dim3(row_blocks(M, num_sms)), 256, 0, stream, dy, (uint16_t*)nullptr,
-                                       row_scale, (long long)M, N, 13);
+    using Scale = void (*)(const uint16_t*, const uint16_t*, float*, long long, int);
+    using Long = void (*)(const uint16_t*, const uint16_t*, uint16_t*, const float*, float*, long long, int, int);
+    Scale scale = nullptr;
+    Long fn = nullptr;
+#define W4A16_DP(ACT) \
+    case ACT: scale = dp_scale_kernel<ACT>; fn = linear_dp_long_kernel<ACT>; break
+    switch (act) {
+        W4A16_DP(W4A16_ACT_NONE);
+        W4A16_DP(W4A16_ACT_RELU);
+        W4A16_DP(W4A16_ACT_SILU);
+        W4A16_DP(W4A16_ACT_GELU);
+        W4A16_DP(W4A16_ACT_GELU_TANH);
+        default: return cudaErrorInvalidValue;
+    }
+#undef W4A16_DP
+    const cudaError_t e = launch_after(scale, dim3(row_blocks(M, num_sms)), 512, 0, stream, dy, pre, row_scale, (long long)M, N);
     if (e != cudaSuccess) return e;
     const int rows = (int)((M + runs - 1) / runs);
     const dim3 grid((N + kDpCols - 1) / kDpCols, (unsigned)((M + rows - 1) / rows));
     if (sums != nullptr) *sum_rows = (int)grid.y;
-    auto* fn = act == W4A16_ACT_NONE   ? linear_dp_long_kernel<W4A16_ACT_NONE>
-               : act == W4A16_ACT_RELU ? linear_dp_long_kernel<W4A16_ACT_RELU>
-               : act == W4A16_ACT_SILU ? linear_dp_long_kernel<W4A16_ACT_SILU>
-               : act == W4A16_ACT_GELU ? linear_dp_long_kernel<W4A16_ACT_GELU>
-                                       : linear_dp_long_kernel<W4A16_ACT_GELU_TANH>;
     return launch_after(fn, grid, 32 * kDpRowThreads, 0, stream, dy, pre, dp, (const float*)row_scale, sums, (long long)M, N,
                         rows);
 }
