@@ -498,11 +498,12 @@ cudaError_t launch_gated_dp(const uint16_t* dh, const uint16_t* g, const uint16_
                             int64_t M, int F, int act, int num_sms, unsigned* err, cudaStream_t stream) {
     const bool keep = F <= 16384;  // 512 threads with four chunks each
     const int threads = keep ? (F / 32 + 31) / 32 * 32 : 512;
-    // resident blocks by registers (128 a thread at most), and at least two rows in flight for each
+    // resident blocks by registers (128 a thread at most); two rows of each fit (32 columns per thread, three
+    // sources of 2 bytes)
     constexpr size_t kRing = kRingSmemBytes;
     const size_t row = (size_t)6 * F;
-    int blocks = 512 / threads > 8 ? 8 : 512 / threads;
-    while (keep && blocks > 1 && 2 * blocks * row > kRing) --blocks;
+    static_assert(2 * 512 * 32 * 6 <= kRing, "two rows of every block");
+    const int blocks = 512 / threads > 8 ? 8 : 512 / threads;
     int depth = keep ? (int)(kRing / blocks / row) : 0;
     depth = depth > kDpDepth ? kDpDepth : depth;
     const int64_t cap = (int64_t)num_sms * (keep ? blocks : 4);

@@ -503,10 +503,11 @@ NormPlan norm_plan(int64_t M, int K, int srcs, int num_sms) {
     b.T = norm_threads(K, b.V);
     b.grid = (int)(M < (int64_t)num_sms * 65536 ? M : (int64_t)num_sms * 65536);
     if (!many) return b;
-    // resident blocks by threads (at up to 112 registers each), then the ring's depth by shared memory
+    // resident blocks by threads (at up to 112 registers each), then the ring's depth by shared memory: where an
+    // SM has several blocks, two rows of each fit (32 channels per thread, two sources of 2 bytes)
+    static_assert(2 * 576 * 32 * 4 <= kRingBytes, "two rows of every block");
     int blocks = 576 / b.T < 1 ? 1 : 576 / b.T > 8 ? 8 : 576 / b.T;
     const size_t row = (size_t)2 * K * srcs;
-    while (blocks > 1 && (size_t)blocks * 2 * row > kRingBytes) --blocks;
     b.depth = (int)(kRingBytes / blocks / row);
     b.depth = b.depth < 1 ? 1 : b.depth > kMaxDepth ? kMaxDepth : b.depth;
     b.smem = b.depth * row;
@@ -553,8 +554,9 @@ NormBwdPlan norm_backward_many(int64_t M, int K, int srcs, int num_sms, int V) {
     const int64_t need = (M + b.groups - 1) / b.groups;
     b.grid = (int)(need < num_sms ? need : num_sms);
     const size_t row = (size_t)2 * K * srcs;
-    // at least two rows: one is filled while the other is read
-    while (b.groups > 1 && 2 * b.groups * row > kRingBytes) --b.groups;
+    // at least two rows, one filled while the other is read: several groups always have them (32 channels per
+    // thread at most, three sources of 2 bytes)
+    static_assert(2 * 512 * 32 * 6 <= kRingBytes, "two rows of every group");
     b.depth = (int)(kRingBytes / b.groups / row);
     b.depth = b.depth > kMaxDepth ? kMaxDepth : b.depth;
     if (b.depth < 2) b.depth = 0;  // rows too long: the threads load them themselves
