@@ -4,8 +4,10 @@
 //   GELU       p Phi(p);               derivative Phi + p phi,          Phi = (1 + erf(p / sqrt 2)) / 2
 //   GELU_TANH  p (1 + tanh z) / 2 = p sg(2 z), z = sqrt(2 / pi) (p + 0.044715 p^3);
 //              derivative sg + p sg (1 - sg) 2 z'
-// The sigmoid is 1 / (1 + e^-p) by the fast exponential and division (relative error below 2^-20,
-// far inside the bf16 rounding that every result goes through).  It saturates without a NaN: e^-p
+// The sigmoid is 1 / (1 + e^-p) by the fast exponential, within 2 + 1.173 |p| units of its last place, and the
+// fast division, within 2.  For p >= 0 that is a relative error below 2^-20; for negative p, where e^-p decides,
+// at most (5 + 1.2 |p|) 2^-23 (2^-18 at p = -20, 2^-16 where it underflows), far inside the bf16 rounding that
+// every result goes through.  It saturates without a NaN: e^-p
 // overflows to infinity for p below -88 and 1 / inf is 0, and p * 0 is 0 for every finite p.
 #pragma once
 

@@ -34,7 +34,7 @@
 //     second nibble and not for an fp16 scale: 19 operations, with scale = hi + lo, hi = bf16(scale); lo
 //     has at most 3 bits and q - z 4, so (q - z) lo is exact and fma(q - z, hi, (q - z) lo) rounds once.
 //   - GATED interleaves gate and up rows in sixteens, so the two sums of a channel sit in one warp's
-//     lanes l and l + 16 and meet by a shuffle.
+//     lanes l and l + 16 and meet in its transposing buffer.
 //   - Whole tiles go round the pairs; the tiles that do not fill a round are cut along the contraction
 //     into equal runs, one per pair, whose fp32 partial tiles meet in the workspace: the last to arrive
 //     (at a half of the columns, where the contributors end together) adds them in the order of the runs,
