@@ -500,7 +500,8 @@ w4a16_status w4a16_linear_fused(const uint16_t* x, const w4a16_weights* weights,
  *   pre       [M][N] bf16 bits, as the forward call wrote it.  Ignored, may be NULL, for NONE.
  *   dx        [M][K] bf16 bits, output.  dbias [N] fp32, output, or NULL.
  *   dp enters the product in fp16 over a power of two per token, its largest value at 2^14 or
- *   more (2^-96 or more before the scaling; smaller rows keep fewer bits), and each weight rounded once to fp16: |(q - z) scale| <= 65504, or it is infinite.
+ *   more (tokens whose largest |dp| is below 2^-96 keep fewer bits), and each weight rounded
+ *   once to fp16: |(q - z) scale| <= 65504, or it is infinite.
  *   dbias sums the unrounded fp32 dp.
  *   workspace: required, W4A16_OP_LINEAR_BACKWARD.  Repeated calls give the same bits.
  *   Errors: as w4a16_linear_fused.
@@ -517,8 +518,8 @@ w4a16_status w4a16_linear_fused_backward(const uint16_t* dy, const uint16_t* pre
  *   g_out, u_out  [M][F] bf16 bits, outputs, or both NULL: bf16_rne(g), bf16_rne(u), for the
  *                 backward pass.
  *   For M > 16 the operands are fp16 as in w4a16_linear_fused_backward: x over a power of two
- *   per token, which keeps every bf16 value above 2^-28 of the token's largest as it is, and
- *   weights rounded once, |(q - z) scale| <= 65504.
+ *   per token, which keeps every bf16 value above 2^-28 of the token's largest as it is (for a
+ *   largest one of 2^-96 or more), and weights rounded once, |(q - z) scale| <= 65504.
  *   workspace: required, W4A16_OP_GATED with N = F.  Otherwise as w4a16_linear_fused (NULL also
  *   when only one of g_out and u_out is given).
  */
@@ -545,7 +546,8 @@ w4a16_status w4a16_gated_backward(const uint16_t* dh, const uint16_t* g, const u
  *   or NULL for no fold: y is then the norm itself.
  *   residual  or NULL: h is then x.   h: output, or NULL when it is not wanted; it may be x or
  *             residual (the addition in place).  y may be x or residual when h is another buffer.
- *   The statistics and v = h * rstd * weight / s are fp32.
+ *   The statistics and v = h * rstd * weight / s are fp32: the sum of a row's squares has to be
+ *   below 2^128, and with eps = 0 their mean above 2^-126 (a row of zeros gives NaN then).
  *   1 <= M <= 2^24; K a multiple of 8, 8 <= K <= 32768; eps finite and >= 0 (VALUE).  Every
  *   pointer 16-byte aligned.  No workspace.
  */
@@ -558,7 +560,8 @@ w4a16_status awq_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint
  * that v is about q * scale (v as in awq_rmsnorm, fp32).
  *   q [M][K] bytes (E4M3); scales [M][K/group_size] fp32.  group_size: K (one scale per row) or a
  *   multiple of 128 that divides K.  A NaN in a group makes its scale and codes NaN; an infinity
- *   makes the scale infinite, the infinite entries' codes NaN and the others 0.
+ *   makes the scale infinite, the infinite entries' codes NaN and the others 0.  So does a
+ *   product h * weight / s beyond the range of fp32.
  *   Everything else as awq_rmsnorm.
  */
 w4a16_status awq_rmsnorm_e4m3(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const float* s,
