@@ -67,6 +67,43 @@ def test_two_widths(calls, widths):
     w4.check_device_status()
 
 
+@pytest.mark.parametrize("M", [40, 400])
+def test_two_threads_on_one_stream(M):
+    """The calls of two threads on the same stream, on different operands: each call is more than one launch, and the
+    threads' launches may alternate."""
+    N, K = 2048, 1024
+
+    def calls(seed):
+        layer, up = (tuple(t.cuda() for t in ref.pack_layer(seed + i, N, K)[0]) for i in (0, 1))
+        a, b, c = (ref.bf(seed + i, M, N).cuda() for i in range(3))
+        x = ref.bf(seed + 5, M, K).cuda()
+        return [lambda: w4.w4a16_linear_fused_backward(a, *layer, pre=b, activation="gelu", bias_grad=True)[0],
+                lambda: w4.w4a16_gated_backward(a, b, c, layer, up), lambda: w4.w4a16_gated(x, layer, up)]
+    sets = [calls(10), calls(30)]
+    want = [[f().clone() for f in fs] for fs in sets]
+    torch.cuda.synchronize()
+    stream, start, errors, outs = torch.cuda.Stream(), threading.Barrier(2), [], [[], []]
+
+    def work(i):
+        try:
+            with torch.cuda.stream(stream):
+                start.wait(60)
+                for _ in range(200):
+                    outs[i].append([f() for f in sets[i]])
+        except BaseException as e:  # handed to the test's thread
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not any(t.is_alive() for t in threads) and not errors, errors
+    torch.cuda.synchronize()
+    w4.check_device_status()
+    for turns, expected in zip(outs, want):
+        assert all(torch.equal(g.view(torch.int16), w.view(torch.int16)) for turn in turns for g, w in zip(turn, expected))
+
+
 @pytest.mark.skipif(shutil.which("gcc") is None or not os.path.exists(os.path.join(CUDA, "include", "cuda_runtime.h")),
                     reason="no host C compiler or no CUDA toolkit headers")
 @pytest.mark.parametrize("what", ["operators", "quantize"])

@@ -37,6 +37,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -284,10 +285,11 @@ _workspaces = {}
 def workspace(device: torch.device, nbytes: int, stream=None) -> torch.Tensor:
     """A zero-filled device workspace of at least nbytes for calls on `stream` of `device`,
     cached so that consecutive calls on the same stream reuse it (each call leaves it zeroed).
-    Calls on different streams get different workspaces."""
+    Calls on different streams get different workspaces, and so do calls of different host threads:
+    the launches of two threads' calls may alternate on one stream."""
     dev = torch.device(device)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
-    key = (dev.index if dev.index is not None else torch.cuda.current_device(), s.cuda_stream)
+    key = (dev.index if dev.index is not None else torch.cuda.current_device(), s.cuda_stream, threading.get_ident())
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
@@ -563,7 +565,7 @@ _fused_bytes = {}
 
 
 def _fused_workspace(ws, device, stream, op, M, N, K):
-    """(address, bytes) of the caller's workspace, or of the cached one of the current stream.  While
+    """(address, bytes) of the caller's workspace, or of the cached one of the current stream and thread.  While
     the stream is being captured: of one of the graph's own, its counters zeroed by the graph, so
     that graphs share none and a later call that needs a larger one takes nothing from under a
     graph."""
@@ -581,7 +583,7 @@ def _fused_workspace(ws, device, stream, op, M, N, K):
         ws = torch.empty(max(nbytes, _WORKSPACE_ZERO_BYTES), dtype=torch.uint8, device=device)
         ws[:_WORKSPACE_ZERO_BYTES].zero_()
     else:
-        ws = _workspaces.get((device.index, stream))
+        ws = _workspaces.get((device.index, stream, threading.get_ident()))
         if ws is None or ws.numel() < nbytes:
             ws = workspace(device, nbytes)
     return ws.data_ptr(), ws.numel()
