@@ -42,8 +42,8 @@
 //     behind whole tiles.  No pair waits for another.
 //   - Bound: with many tokens the tensor pipe, 96 % busy (4096 tokens, K 4096, F 14336: 598 us alone, 1.61
 //     PFLOP/s; 706 to 742 us in a row of calls, at the clock that the power limit leaves).  With few, the
-//     loads and the dequant, about as long as one another (32 tokens, 16384 x 18944: 61 us, 2.5 TB/s of
-//     packed weights; 56 us with the dequant's arithmetic left out).
+//     loads and the dequant, about as long as one another (32 tokens, 16384 x 18944: 67 us, 2.4 TB/s of
+//     packed weights; an early form 61 us, and 56 us with the dequant's arithmetic left out).
 //   - Every wait on an mbarrier is bounded; one that runs out records kErrTimeout and its role stops.  The
 //     epilogue warps, which also meet at a barrier of their own, stop together.  All roles of both CTAs then
 //     meet at the closing cluster barrier.

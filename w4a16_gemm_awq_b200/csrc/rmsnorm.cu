@@ -10,7 +10,7 @@
 //   - Many rows: a block walks rows that bulk copies bring into a ring in shared memory, so the loads of
 //     the next rows are in flight whatever the threads do with the current one (loads issued by the
 //     threads themselves, one row at a time: e4m3 1999 x 5120 26.6 us, backward 4096 x 4096 38.8 us;
-//     with the ring 16.4 us and 32.5 us, 4.4 and 4.1 TB/s; 8192 x 8192 in bf16 94 us, 5.7 TB/s of the
+//     with the ring 16.4 us and 32.7 us, 4.4 and 4.1 TB/s; 8192 x 8192 in bf16 94 us, 5.7 TB/s of the
 //     6.55 that a copy reaches).  A thread holds 4 chunks of 8 channels of the row (backward 2 or 4),
 //     packed as bf16 (the sum h is exact there), and weight / s.
 //   - Few rows: one block per row with as many threads as it has chunks, which shortens its latency.
