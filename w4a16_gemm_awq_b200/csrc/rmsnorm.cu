@@ -101,7 +101,10 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*buf)[32], int t
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
     const int warps = threads >> 5;
-    if (warps == 1) return;
+    if (warps == 1) {
+        __syncwarp();  // orders memory as the barrier does for more warps: a ring slot may be refilled after it
+        return;
+    }
     if ((t & 31) == 0) {
 #pragma unroll
         for (int i = 0; i < N; ++i) buf[i][t >> 5] = v[i];
